@@ -108,6 +108,15 @@ def load_library():
     lib.dq_solve_batched.restype = I
     lib.dq_act_quant.argtypes = [P, I, I64, I64, P, I, I, I, ctypes.POINTER(_Outputs), P, SZ, P]
     lib.dq_act_quant.restype = I
+    lib.dq_matmul.argtypes = [ctypes.POINTER(_Outputs), I64, ctypes.POINTER(_Outputs), I64, I64, I, I, P, I, P, SZ, P]
+    lib.dq_matmul.restype = I
+    lib.dq_norm_workspace_bytes.argtypes = [I64, I64, I, I]
+    lib.dq_norm_workspace_bytes.restype = SZ
+    lib.dq_norm_quant.argtypes = [P, P, I, I64, I64, P, ctypes.c_float, P, I, I, I, ctypes.POINTER(_Outputs), P, P, SZ,
+                                  P]
+    lib.dq_norm_quant.restype = I
+    lib.dq_glu_quant.argtypes = [P, P, I, I64, I64, I64, P, I, I, I, ctypes.POINTER(_Outputs), P, SZ, P]
+    lib.dq_glu_quant.restype = I
     lib.dq_status_str.argtypes = [I]
     lib.dq_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -345,6 +354,215 @@ def dq_act_quant(X: torch.Tensor, col_scales: torch.Tensor, fmt, group: Optional
         st = lib.dq_sync_status(workspace.data_ptr(), _stream_ptr(stream))
         if st != 0:
             raise DQError(st, "dq_act_quant (device)")
+    out["workspace"] = workspace
+    return out
+
+
+class _on:
+    """The device of the call's tensors as the current one, and ``stream`` (default: that device's current
+    stream) as the stream that new outputs and workspaces belong to."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        self.guards = []
+        if self.device.index is not None and torch.cuda.current_device() != self.device.index:
+            self.guards.append(torch.cuda.device(self.device))
+        if self.stream is not None:
+            self.guards.append(torch.cuda.stream(self.stream))
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _quantized(t: dict, rows: Optional[int], cols: Optional[int], f: Format, device, where: str) -> tuple:
+    """(rows, cols) of a quantized matrix {"codes", "block_scales", "tensor_scale"}; DQError unless its tensors
+    are the format's, on `device`."""
+    codes, scales = t["codes"], t["block_scales"]
+    if codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.device != device:
+        raise DQError(1, where + ": codes must be a contiguous 2-D uint8 tensor on the call's device")
+    r, c = codes.shape[0], codes.shape[1] * (1 if f == Format.MXFP8 else 2)
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise DQError(1, where + ": codes [%d][%d columns] do not fit the call" % (r, c))
+    if (scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.device != device
+            or tuple(scales.shape) != (r, c // DEFAULT_GROUP[f])):
+        raise DQError(1, where + ": block_scales must be contiguous uint8 [rows][cols/group] on the call's device")
+    if f == Format.NVFP4:
+        s = t.get("tensor_scale")
+        if s is None or s.dtype != torch.float32 or s.numel() != 1 or s.device != device:
+            raise DQError(1, where + ": NVFP4 needs a one-element float32 tensor_scale on the call's device")
+    return r, c
+
+
+def _quantized_struct(t: dict, f: Format) -> _Outputs:
+    s = t.get("tensor_scale")
+    return _Outputs(t["codes"].data_ptr(), t["block_scales"].data_ptr(),
+                    s.data_ptr() if f == Format.NVFP4 or s is not None else None, None, None)
+
+
+def _product_format(fmt, group: Optional[int], where: str) -> Format:
+    f = _fmt(fmt)
+    if f not in (Format.NVFP4, Format.MXFP4, Format.MXFP8):
+        raise DQError(2, where + ": nvfp4, mxfp4 and mxfp8 only")
+    if group is not None and group != DEFAULT_GROUP[f]:
+        raise DQError(2, where + ": group %d" % DEFAULT_GROUP[f])
+    return f
+
+
+def _workspace_for(workspace: Optional[torch.Tensor], nbytes: int, device, where: str) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise DQError(1, where + ": workspace must be a contiguous uint8 tensor on the call's device")
+    return workspace
+
+
+def _raise_device_status(lib, workspace: torch.Tensor, stream_ptr: int, where: str):
+    st = lib.dq_sync_status(workspace.data_ptr(), stream_ptr)
+    if st != 0:
+        raise DQError(st, where + " (device)")
+
+
+MATMUL_WORKSPACE_BYTES = 256
+
+
+def dq_matmul(X: dict, W: dict, fmt, group: Optional[int] = None, out: Optional[torch.Tensor] = None,
+              out_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None, stream=None,
+              check: bool = True) -> torch.Tensor:
+    """Enqueue dq_matmul: Y [tokens, rows] = quantized activations X times the transposed quantized weights W.
+
+    X and W are dicts with "codes", "block_scales" and (NVFP4) "tensor_scale", as dq_act_quant, dq_norm_quant,
+    dq_glu_quant and dq_solve return them, both in ``fmt`` (nvfp4, mxfp4 or mxfp8).  ``out`` (its dtype then
+    counts, not ``out_dtype``) and ``workspace`` keep the call free of allocations; ``check`` waits for the
+    stream and raises on a device-reported status."""
+    lib = load_library()
+    f = _product_format(fmt, group, "dq_matmul")
+    if not X["codes"].is_cuda:
+        raise DQError(1, "dq_matmul: X must be on a CUDA device")
+    dev = X["codes"].device
+    tokens, cols = _quantized(X, None, None, f, dev, "dq_matmul: X")
+    rows, _ = _quantized(W, None, cols, f, dev, "dq_matmul: W")
+    with _on(dev, stream) as sp:
+        if out is None:
+            if out_dtype not in _DTYPES:
+                raise DQError(1, "dq_matmul: out_dtype must be float32, bfloat16 or float16")
+            out = torch.empty((tokens, rows), dtype=out_dtype, device=dev)
+        elif out.dtype not in _DTYPES or tuple(out.shape) != (tokens, rows) or not out.is_contiguous() or out.device != dev:
+            raise DQError(1, "dq_matmul: out must be contiguous f32/bf16/f16 [tokens, rows] on the call's device")
+        workspace = _workspace_for(workspace, MATMUL_WORKSPACE_BYTES, dev, "dq_matmul")
+        xo, wo = _quantized_struct(X, f), _quantized_struct(W, f)
+        st = lib.dq_matmul(ctypes.byref(xo), tokens, ctypes.byref(wo), rows, cols, int(f), DEFAULT_GROUP[f],
+                           out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(), workspace.numel(), sp)
+        if st != 0:
+            raise DQError(st, "dq_matmul")
+        if check:
+            _raise_device_status(lib, workspace, sp, "dq_matmul")
+    return out
+
+
+def _row_outputs(out: Optional[dict], rows: int, cols: int, f: Format, device, where: str) -> dict:
+    if out is None:
+        g = DEFAULT_GROUP[f]
+        return {"codes": torch.empty((rows, code_cols(cols, f)), dtype=torch.uint8, device=device),
+                "block_scales": torch.empty((rows, cols // g), dtype=torch.uint8, device=device),
+                "tensor_scale": torch.empty(1, dtype=torch.float32, device=device)}
+    _quantized(out, rows, cols, f, device, where)
+    return out
+
+
+def _channel_vector(t: Optional[torch.Tensor], cols: int, dtypes, device, where: str):
+    if t is not None and (t.dtype not in dtypes or t.numel() != cols or not t.is_contiguous() or t.device != device):
+        raise DQError(1, where + " must be a contiguous 16-bit float [cols] tensor on the call's device")
+    return None if t is None else t.data_ptr()
+
+
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: Optional[torch.Tensor], fmt,
+                  residual: Optional[torch.Tensor] = None, eps: float = 1e-5, group: Optional[int] = None,
+                  out: Optional[dict] = None, residual_out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None, check: bool = True) -> dict:
+    """Enqueue dq_norm_quant: h = X + residual (if given), its RMS norm times ``weight`` and the column inverse
+    scales, quantized row-wise in ``fmt`` (mxfp8, mxfp4 or nvfp4).  Returns the quantized matrix with
+    out["residual"] = h (with a residual; ``residual_out`` may be X or the residual itself).  A non-finite row
+    gets NaN scales; ``check`` waits and raises on it."""
+    lib = load_library()
+    f = _product_format(fmt, group, "dq_norm_quant")
+    if not X.is_cuda or X.dtype not in _HALVES or not X.is_contiguous() or X.dim() != 2:
+        raise DQError(1, "dq_norm_quant: X must be a contiguous 2-D bf16/f16 CUDA tensor")
+    rows, cols = X.shape
+    dev = X.device
+    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
+        if t is not None and (t.dtype != X.dtype or t.shape != X.shape or not t.is_contiguous() or t.device != dev):
+            raise DQError(1, "dq_norm_quant: %s must match X" % name)
+    if residual is None and residual_out is not None:
+        raise DQError(1, "dq_norm_quant: residual_out without a residual")
+    gp = _channel_vector(weight, cols, (X.dtype,), dev, "dq_norm_quant: weight (in X's dtype)")
+    bp = _channel_vector(col_scales, cols, _HALVES, dev, "dq_norm_quant: col_scales")
+    with _on(dev, stream) as sp:
+        nbytes = lib.dq_norm_workspace_bytes(rows, cols, int(f), DEFAULT_GROUP[f])
+        if nbytes == 0:
+            raise DQError(1, "dq_norm_workspace_bytes")
+        out = _row_outputs(out, rows, cols, f, dev, "dq_norm_quant: out")
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(X)
+        workspace = _workspace_for(workspace, nbytes, dev, "dq_norm_quant")
+        o = _quantized_struct(out, f)
+        st = lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), _DTYPES[X.dtype], rows,
+                               cols, gp, eps, bp, 1 if col_scales is None else _DTYPES[col_scales.dtype], int(f),
+                               DEFAULT_GROUP[f], ctypes.byref(o),
+                               None if residual_out is None else residual_out.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), sp)
+        if st != 0:
+            raise DQError(st, "dq_norm_quant")
+        if check:
+            _raise_device_status(lib, workspace, sp, "dq_norm_quant")
+    if residual is not None:
+        out["residual"] = residual_out
+    out["workspace"] = workspace
+    return out
+
+
+def dq_glu_quant(X, col_scales: Optional[torch.Tensor], fmt, group: Optional[int] = None, out: Optional[dict] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None, check: bool = True) -> dict:
+    """Enqueue dq_glu_quant: silu(gate) * up times the column inverse scales, quantized row-wise in ``fmt``
+    (mxfp8, mxfp4 or nvfp4).  X is one tensor [tokens, 2 cols], gate left of up (a product over stacked gate and
+    up weights), or a pair (gate, up) of [tokens, cols] tensors with one row stride."""
+    lib = load_library()
+    f = _product_format(fmt, group, "dq_glu_quant")
+    if isinstance(X, torch.Tensor):
+        if X.dim() != 2 or X.shape[1] % 2 != 0:
+            raise DQError(1, "dq_glu_quant: X must be 2-D with an even number of columns")
+        gate, up = X[:, :X.shape[1] // 2], X[:, X.shape[1] // 2:]
+    else:
+        gate, up = X
+    for t in (gate, up):
+        if not t.is_cuda or t.dtype not in _HALVES or t.dim() != 2 or t.stride(1) != 1:
+            raise DQError(1, "dq_glu_quant: gate and up must be 2-D bf16/f16 CUDA tensors with adjacent columns")
+    if gate.shape != up.shape or gate.dtype != up.dtype or gate.device != up.device or (
+            gate.shape[0] > 1 and gate.stride(0) != up.stride(0)):
+        raise DQError(1, "dq_glu_quant: gate and up must agree in shape, dtype, device and row stride")
+    rows, cols = gate.shape
+    ld = gate.stride(0) if rows > 1 else cols
+    dev = gate.device
+    bp = _channel_vector(col_scales, cols, _HALVES, dev, "dq_glu_quant: col_scales")
+    with _on(dev, stream) as sp:
+        out = _row_outputs(out, rows, cols, f, dev, "dq_glu_quant: out")
+        workspace = _workspace_for(workspace, ACT_WORKSPACE_BYTES, dev, "dq_glu_quant")
+        o = _quantized_struct(out, f)
+        st = lib.dq_glu_quant(gate.data_ptr(), up.data_ptr(), _DTYPES[gate.dtype], rows, cols, ld, bp,
+                              1 if col_scales is None else _DTYPES[col_scales.dtype], int(f), DEFAULT_GROUP[f],
+                              ctypes.byref(o), workspace.data_ptr(), workspace.numel(), sp)
+        if st != 0:
+            raise DQError(st, "dq_glu_quant")
+        if check:
+            _raise_device_status(lib, workspace, sp, "dq_glu_quant")
     out["workspace"] = workspace
     return out
 

@@ -298,6 +298,74 @@ int dq_act_quant(const void* X, int x_dtype, int64_t rows, int64_t cols, const v
                  int format, int group, const dq_outputs* out, void* workspace, size_t workspace_bytes,
                  void* stream);
 
+/* Workspace bytes of dq_matmul (header only). */
+#define DQ_MATMUL_WORKSPACE_BYTES 256u
+
+/* The product of quantized activations and a quantized weight matrix
+ * (DualQuant summary §4.4: X W^T = (X D_b) Q^T D_a, with b folded into the
+ * activations by dq_act_quant, dq_norm_quant or dq_glu_quant):
+ *   Y[t][n] = s_x s_w sum_k (a_x q_x)[t][k] (a_w q_w)[n][k]
+ * X  codes [tokens][..] and block_scales [tokens][cols/group] of the
+ *    activations, W those of the weights [rows][cols] (a dq_solve or dq_rtn
+ *    result), both in `format`; tensor_scale of both for DQ_NVFP4 (not read
+ *    otherwise); col_scales and mse are not used.
+ * Y  [tokens][rows], densely packed, y_dtype DQ_F32, DQ_BF16 or DQ_F16; it must
+ *    not overlap the operands.
+ * Formats DQ_NVFP4, DQ_MXFP4 and DQ_MXFP8; the integer grids return
+ * DQ_EUNSUPPORTED.  cols is a multiple of the group, the other sizes are any
+ * from 1.  Products of codes and scales are exact, sums are fp32 and rounded
+ * once to y_dtype; a value beyond its range becomes an infinity.  A NaN block
+ * scale (E8M0 0xFF, E4M3 0x7F) makes its row's outputs NaN and no others.  The
+ * order of a sum depends on the shape alone, so equal calls give equal bits.
+ * Codes that are 16-byte aligned in every row (16-byte aligned pointers and,
+ * in the 4-bit formats, cols a multiple of 32) take the tensor-core kernels;
+ * others take a slower kernel.
+ * The workspace (DQ_MATMUL_WORKSPACE_BYTES, 256-byte aligned) reports a bounded
+ * wait that ran out through dq_sync_status (DQ_ECUDA).  Calls that may run at
+ * the same time need a workspace each. */
+int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format, int group,
+              void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device workspace bytes of dq_norm_quant (0 on invalid arguments): a header
+ * and, for DQ_NVFP4, 8 bytes per row.  Alignment: 256 bytes. */
+size_t dq_norm_workspace_bytes(int64_t rows, int64_t cols, int format, int group);
+
+/* Root-mean-square norm with the residual's addition, quantized for a product
+ * whose weights have column scales b, in one pass:
+ *   h  = X + residual                 rounded to x_dtype, written to residual_out
+ *   x' = h / sqrt(mean_row(h^2) + eps) * weight * b
+ *   a  = Proj_Fa(max|x'| over the group / qmax), 1 for an all-zero group
+ *   q  = Q(x' / a)                    nearest grid value, ties to even, clipped
+ * X [rows][cols] (rows = tokens), x_dtype DQ_BF16 or DQ_F16.  residual is NULL
+ * (h = X, residual_out NULL too) or [rows][cols]; residual_out may be X's or the
+ * residual's own buffer.  weight [cols] in x_dtype and col_scales [cols] in
+ * col_dtype (DQ_BF16 or DQ_F16) may be NULL (ones).  eps >= 0.
+ * x' is not rounded before the quantization: scales and codes are those of the
+ * fp64 values.  Formats: DQ_MXFP8 (8-bit codes), DQ_MXFP4 and DQ_NVFP4, whose
+ * tensor scale is fp32(amax|x'| / 2688) over the call (1 if all are 0); others
+ * return DQ_EUNSUPPORTED.  Outputs as for dq_act_quant.
+ * A value of x' that is NaN or beyond fp32's range gives its group the format's
+ * NaN scale (E8M0 0xFF, E4M3 0x7F) and zero codes, takes no part in the tensor
+ * scale, and dq_sync_status reports DQ_ENONFINITE; every other group is valid.
+ * A NaN or an infinity in h makes its whole row such.
+ * X, residual, residual_out and weight 16-byte aligned, codes 8-byte aligned. */
+int dq_norm_quant(const void* X, const void* residual, int x_dtype, int64_t rows, int64_t cols, const void* weight,
+                  float eps, const void* col_scales, int col_dtype, int format, int group, const dq_outputs* out,
+                  void* residual_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gated activation between the two products of an MLP, quantized for the
+ * second:
+ *   x' = gate / (1 + exp(-gate)) * up * b
+ * with scales and codes as for dq_norm_quant, formats, non-finite values and
+ * col_scales (may be NULL) too.  gate and up [rows][cols] in x_dtype (DQ_BF16 or
+ * DQ_F16) share the row stride `ld` in elements (ld >= cols, a multiple of 8):
+ * the two halves of one product's output [rows][2 cols] are gate, gate + cols
+ * and ld = 2 cols.  Both 16-byte aligned, codes 8-byte aligned; workspace
+ * DQ_ACT_WORKSPACE_BYTES, 256-byte aligned. */
+int dq_glu_quant(const void* gate, const void* up, int x_dtype, int64_t rows, int64_t cols, int64_t ld,
+                 const void* col_scales, int col_dtype, int format, int group, const dq_outputs* out, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
 /* Size of the library-owned device scratch that dq_solve_static uses: 8 MiB.
  * A shape fits when dq_workspace_bytes(rows, cols, format, group) is at most
  * this.  The workspace holds the working block scales (rows x cols/group
