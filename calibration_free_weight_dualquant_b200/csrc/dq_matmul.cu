@@ -7,11 +7,16 @@
 // the column scales b are in q_x already).  Sums are held in fp32 and rounded
 // once, after the tensor scales, to the output type.
 #include <climits>
+#include <cstring>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
 
 #include "dq.h"
 #include "dq_device.cuh"
 #include "dq_fast.cuh"
 #include "dq_internal.h"
+#include "dq_tc.cuh"
 
 namespace dq {
 
@@ -82,6 +87,7 @@ __global__ void __launch_bounds__(256) k_matmul_any(MatmulProblem p) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int64_t tiles_n = (p.N + 63) / 64, nb = p.K / G;
   const int64_t t0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * 64;
+  if (blockIdx.x == 0 && tid == 0) p.hdr->flags = 0;
   float acc[4][4] = {};
   for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
 #pragma unroll
@@ -139,6 +145,349 @@ static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Tensor-core product: a CTA computes the tile of 128 output features and BN
+// tokens, Y^T = W X^T, so that few tokens still fill the tensor core's 128
+// rows.  Codes go by TMA into 128-byte-swizzled shared memory as they are
+// stored; block scales are read as stored, one row's bytes of a K tile a lane,
+// and written to shared memory transposed into the words that tcgen05.cp moves
+// to tensor memory; tcgen05.mma multiplies codes and scales and sums in fp32
+// in tensor memory.  Where there are fewer tiles than SMs the columns are
+// split over the CTAs of a cluster, whose partial tiles are joined through
+// distributed shared memory in rank order (no atomics: equal calls give equal
+// bits).
+//
+// Warps: 0 issues the copies, 1 the tensor-core work; 2 .. 4 bring scales and,
+// with 5, write the tile out (warp w reads tensor-memory lanes 32 (w % 4) ..).
+constexpr int kMmThreads = 192;
+constexpr int kMmMaxStages = 8;
+
+template <int FMT, int BN>
+struct MmGeo {
+  using F = TcFormat<FMT>;
+  static constexpr int kHalves = (BN + 127) / 128;  // 128-row blocks of the token scales
+  static constexpr int kA = 128 * 128, kB = BN * 128;
+  static constexpr int kSfA = F::kAtoms * 512, kSfB = F::kAtoms * 512 * kHalves;
+  static constexpr int kStage = (kA + kB + kSfA + kSfB + 1023) / 1024 * 1024;
+  static constexpr int kAccCols = BN < 32 ? 32 : BN;
+  static constexpr int kSfACol = kAccCols, kSfBCol = kAccCols + 16;
+  static constexpr int kCols = kAccCols + 16 + 16 * kHalves;
+  static constexpr int kAlloc = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
+};
+
+// Block scales of the K tile `kt` for the lane's four rows (row0 + lane + 32 q)
+// as words w[q][atom]; zeros past the matrix.  U: bytes a load, a divisor of
+// the row's bytes, so no load straddles the row's end.
+template <int FMT, int U>
+__device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t kt,
+                                            uint32_t (*w)[TcFormat<FMT>::kAtoms]) {
+  constexpr int SB = TcFormat<FMT>::kScaleBytes, A = TcFormat<FMT>::kAtoms;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t r = row0 + (threadIdx.x & 31) + 32 * q;
+    const unsigned char* p = s + r * nb + kt * SB;
+    const int64_t left = r < rows ? nb - kt * SB : 0;
+#pragma unroll
+    for (int j = 0; j < A; ++j) w[q][j] = 0;
+#pragma unroll
+    for (int i = 0; i < SB / U; ++i) {
+      if (i * U < left) {
+        if constexpr (U == 16) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+          w[q][0] = v.x, w[q][A > 1 ? 1 : 0] = v.y, w[q][A > 2 ? 2 : 0] = v.z, w[q][A > 3 ? 3 : 0] = v.w;
+        } else if constexpr (U == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
+          w[q][2 * i] = v.x, w[q][A > 1 ? 2 * i + 1 : 0] = v.y;
+        } else if constexpr (U == 4) {
+          w[q][i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+        } else if constexpr (U == 2) {
+          w[q][i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) << (16 * (i & 1));
+        } else {
+          w[q][i / 4] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
+        }
+      }
+    }
+  }
+}
+
+// Bounded wait for a ring barrier, by the clock alone: the header's flags may
+// still hold what the workspace held before this launch.
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned* flags) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_ns() - t0 > kWaitLimitNs) {
+      atomicOr(flags, kFlagTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+// A warp brings one 128-row block's scales of the K tiles k0 .. k0 + n - 1 into
+// the ring, kAhead tiles ahead in registers.
+constexpr int kAhead = 4;
+template <int FMT, int U>
+__device__ __forceinline__ void scale_loop(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t k0, int n,
+                                           unsigned char* ring, int stage_bytes, int stages, int atom_bytes,
+                                           uint64_t* full, uint64_t* empty, unsigned* flags) {
+  constexpr int A = TcFormat<FMT>::kAtoms;
+  const int lane = threadIdx.x & 31;
+  uint32_t w[kAhead][4][A];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u)
+    if (u < n) load_scales<FMT, U>(s, row0, rows, nb, k0 + u, w[u]);
+  int slot = 0;
+  unsigned phase = 1;
+#pragma unroll 1
+  for (int base = 0; base < n; base += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int it = base + u;
+      if (it < n) {
+        if (!__all_sync(0xffffffffu, mm_wait(&empty[slot], phase, flags))) return;
+        unsigned char* dst = ring + slot * stage_bytes + lane * 16;
+#pragma unroll
+        for (int j = 0; j < A; ++j)
+          *reinterpret_cast<uint4*>(dst + j * atom_bytes) = make_uint4(w[u][0][j], w[u][1][j], w[u][2][j], w[u][3][j]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[slot]);
+        if (it + kAhead < n) load_scales<FMT, U>(s, row0, rows, nb, k0 + it + kAhead, w[u]);
+        if (++slot == stages) slot = 0, phase ^= 1;
+      }
+    }
+  }
+}
+template <int FMT, typename... Args>
+__device__ __forceinline__ void scale_warp(int unit, Args... args) {
+  if (unit >= TcFormat<FMT>::kScaleBytes)
+    scale_loop<FMT, TcFormat<FMT>::kScaleBytes>(args...);
+  else if (unit >= 4)
+    scale_loop<FMT, 4>(args...);
+  else if (unit == 2)
+    scale_loop<FMT, 2>(args...);
+  else
+    scale_loop<FMT, 1>(args...);
+}
+
+struct MmLaunch {
+  int split;    // CTAs of a cluster, each with its share of the K tiles
+  int stages;   // ring slots
+  int unit_x, unit_w;  // bytes that a scale load may take: the alignment of pointer and row
+};
+
+template <int FMT, int BN>
+__global__ void __launch_bounds__(kMmThreads, 2)
+    k_matmul_tc(MatmulProblem p, MmLaunch l, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+  using G = MmGeo<FMT, BN>;
+  using F = TcFormat<FMT>;
+  extern __shared__ unsigned char mm_smem[];
+  __shared__ uint64_t full_t[kMmMaxStages], full_s[kMmMaxStages], empty[kMmMaxStages], acc_full;
+  __shared__ uint32_t tmem_base;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t tiles_n = (p.N + 127) / 128;
+  const int64_t tile = blockIdx.x / l.split;
+  const uint32_t rank = blockIdx.x % l.split;
+  const int64_t n0 = tile % tiles_n * 128, t0 = tile / tiles_n * BN;
+  const int64_t nk = (p.K + F::kTileK - 1) / F::kTileK;
+  const int64_t k0 = nk * rank / l.split;
+  const int n = (int)(nk * (rank + 1) / l.split - k0);  // at least 1: split <= nk
+  unsigned* flags = &p.hdr->flags;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < l.stages; ++i) {
+      mbar_init(&full_t[i], 1);
+      mbar_init(&full_s[i], 1 + G::kHalves);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&acc_full, 1);
+    mbar_fence_init();
+    if (blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
+  }
+  if (warp == 1) tc_alloc<G::kAlloc>(smem_u32(&tmem_base));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int slot = 0, issued = 0;
+      unsigned phase = 1;
+      bool ok = true;
+      for (; issued < n; ++issued) {
+        if (!(ok = mm_wait(&empty[slot], phase, flags))) break;
+        unsigned char* st = ring + slot * G::kStage;
+        mbar_arrive_expect_tx(&full_t[slot], G::kA + G::kB);
+        tma_load_2d(st, &wmap, (int)((k0 + issued) * 128), (int)n0, &full_t[slot]);
+        tma_load_2d(st + G::kA, &xmap, (int)((k0 + issued) * 128), (int)t0, &full_t[slot]);
+        if (++slot == l.stages) slot = 0, phase ^= 1;
+      }
+      if (!ok)  // the copies in flight land before the CTA leaves
+        for (int i = max(0, issued - l.stages); i < issued; ++i) mbar_drain(&full_t[i % l.stages], (i / l.stages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int slot = 0;
+      unsigned phase = 0;
+      for (int it = 0; it < n; ++it) {
+        if (!mm_wait(&full_s[slot], phase, flags) || !mm_wait(&full_t[slot], phase, flags)) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(ring + slot * G::kStage);
+        const uint32_t sfa = st + G::kA + G::kB, sfb = sfa + G::kSfA;
+#pragma unroll
+        for (int j = 0; j < F::kAtoms; ++j) {
+          tc_copy_scales(tmem + G::kSfACol + 4 * j, tc_desc_scales(sfa + 512 * j));
+#pragma unroll
+          for (int h = 0; h < G::kHalves; ++h)
+            tc_copy_scales(tmem + G::kSfBCol + 4 * (j * G::kHalves + h), tc_desc_scales(sfb + 512 * (j * G::kHalves + h)));
+        }
+        const uint64_t da = tc_desc_sw128(st), db = tc_desc_sw128(st + G::kA);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma<FMT>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(128, BN, F::byte(k)), tmem + G::kSfACol + 4 * F::atom(k),
+                      tmem + G::kSfBCol + 4 * G::kHalves * F::atom(k), it > 0 || k > 0);
+        tc_commit(&empty[slot]);
+        if (++slot == l.stages) slot = 0, phase ^= 1;
+      }
+      tc_commit(&acc_full);
+    }
+  } else if (warp == 2) {
+    scale_warp<FMT>(l.unit_w, p.ws, n0, p.N, p.K / F::kGroup, k0, n, ring + G::kA + G::kB, G::kStage, l.stages, 512,
+                    full_s, empty, flags);
+  } else if (warp - 3 < G::kHalves) {
+    const int h = warp - 3;
+    scale_warp<FMT>(l.unit_x, p.xs, t0 + 128 * h, p.T, p.K / F::kGroup, k0, n,
+                    ring + G::kA + G::kB + G::kSfA + 512 * h, G::kStage, l.stages, 512 * G::kHalves, full_s, empty, flags);
+  }
+  __syncwarp();
+
+  // the finished tile: tensor-memory lane = feature, column = token
+  const int tv = (int)min((int64_t)BN, p.T - t0);
+  float f1, f2;
+  tensor_factors(p, f1, f2);
+  bool ok = true;
+  if (warp >= 2) {
+    ok = __all_sync(0xffffffffu, mm_wait(&acc_full, 0, flags));
+    tc_fence_after();
+    const int q = warp & 3;
+    const int64_t nn = n0 + 32 * q + lane;
+    float* part = reinterpret_cast<float*>(ring);  // [token][128 features]: the ring is idle now
+#pragma unroll 1
+    for (int c = 0; c < tv && ok; c += 16) {
+      uint32_t v[16];
+      tc_load16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+      tc_load_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (c + i < tv) {
+          if (l.split > 1)
+            part[(c + i) * 128 + 32 * q + lane] = __uint_as_float(v[i]);
+          else if (nn < p.N)
+            y_store(p.y, p.y_dt, (t0 + c + i) * p.N + nn, __uint_as_float(v[i]) * f1 * f2);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  if (l.split > 1) {
+    cluster_sync();
+    const uint32_t part = smem_u32(ring);
+    const int total = tv * 128;
+    for (int e = (int)rank * kMmThreads + threadIdx.x; e < total; e += l.split * kMmThreads) {
+      float s = 0.f;
+      for (int r = 0; r < l.split; ++r) s += ld_cluster_f32(part + 4 * e, r);
+      const int64_t nn = n0 + (e & 127);
+      if (nn < p.N) y_store(p.y, p.y_dt, (t0 + (e >> 7)) * p.N + nn, s * f1 * f2);
+    }
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tc_dealloc<G::kAlloc>(tmem);
+  }
+}
+
+// 2-D tensor map of a code matrix in bytes: boxes of 128 bytes x `box_rows`
+// rows in the 128-byte swizzle, zeros outside.
+static bool encode_codes(CUtensorMap* map, const unsigned char* q, int64_t row_bytes, int64_t rows, int box_rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return (PFN_cuTensorMapEncodeTiled_v12000) nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint32_t elem_strides[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<unsigned char*>(q), dims, strides, box, elem_strides,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int scale_unit(const unsigned char* s, int64_t nb) {
+  const uintptr_t v = (uintptr_t)s | (uintptr_t)nb | 16u;
+  return (int)(v & (~v + 1));
+}
+
+template <int FMT, int BN>
+static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
+  using G = MmGeo<FMT, BN>;
+  CUtensorMap wmap, xmap;
+  const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
+  if (!encode_codes(&wmap, p.wq, row_bytes, p.N, 128) || !encode_codes(&xmap, p.xq, row_bytes, p.T, BN))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = (p.N + 127) / 128 * ((p.T + BN - 1) / BN);
+  const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
+  MmLaunch l;
+  l.split = 1;
+  while (l.split < 8 && 2 * l.split <= nk && tiles * l.split < sms) l.split *= 2;
+  const int64_t per = (nk + l.split - 1) / l.split;
+  const int room = (BN <= 64 ? 110 : 220) * 1024 / G::kStage;
+  l.stages = (int)(per < room ? per : room);
+  if (l.stages > kMmMaxStages) l.stages = kMmMaxStages;
+  l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
+  l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
+  // the partial tile shares the ring's memory
+  int smem = l.stages * G::kStage;
+  if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
+  smem += 1024;
+  auto kern = k_matmul_tc<FMT, BN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(tiles * l.split));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)l.split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, l, wmap, xmap);
+}
+
+template <int FMT>
+static cudaError_t matmul_fmt(const MatmulProblem& p, int sms, cudaStream_t st) {
+  const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
+  if (((uintptr_t)p.xq | (uintptr_t)p.wq | (uintptr_t)row_bytes) % 16 != 0) return matmul_any<FMT>(p, st);
+  if (p.T <= 16) return matmul_tc<FMT, 16>(p, sms, st);
+  if (p.T <= 32) return matmul_tc<FMT, 32>(p, sms, st);
+  if (p.T <= 64) return matmul_tc<FMT, 64>(p, sms, st);
+  if (p.T <= 128 || (p.N + 127) / 128 * ((p.T + 255) / 256) < sms) return matmul_tc<FMT, 128>(p, sms, st);
+  return matmul_tc<FMT, 256>(p, sms, st);
+}
+
 }  // namespace dq
 
 extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format,
@@ -173,9 +522,11 @@ extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* 
   p.K = cols;
   p.hdr = static_cast<dq::WsHeader*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(dq::WsHeader), s) != cudaSuccess) return DQ_ECUDA;
-  const cudaError_t e = format == DQ_NVFP4   ? dq::matmul_any<dq::FMT_NVFP4>(p, s)
-                        : format == DQ_MXFP4 ? dq::matmul_any<dq::FMT_MXFP4>(p, s)
-                                             : dq::matmul_any<dq::FMT_MXFP8>(p, s);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ECUDA;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DQ_ECUDA;
+  const cudaError_t e = format == DQ_NVFP4   ? dq::matmul_fmt<dq::FMT_NVFP4>(p, sms, s)
+                        : format == DQ_MXFP4 ? dq::matmul_fmt<dq::FMT_MXFP4>(p, sms, s)
+                                             : dq::matmul_fmt<dq::FMT_MXFP8>(p, sms, s);
   return e == cudaSuccess ? DQ_OK : DQ_ECUDA;
 }
