@@ -175,29 +175,31 @@ struct MmGeo {
   static constexpr int kAlloc = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
 };
 
-// Block scales of the K tile `kt` for the lane's four rows (row0 + lane + 32 q)
-// as words w[q][atom]; zeros past the matrix.  U: bytes a load, a divisor of
-// the row's bytes, so no load straddles the row's end.
-template <int FMT, int U>
-__device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t kt,
-                                            uint32_t (*w)[TcFormat<FMT>::kAtoms]) {
-  constexpr int SB = TcFormat<FMT>::kScaleBytes, A = TcFormat<FMT>::kAtoms;
+// Block scales of a lane's four rows (row0 + lane + 32 q): the 32-byte piece
+// `piece` of each row, one memory sector, as words w[q][0 .. 7]; zeros past the
+// matrix.  U: bytes a load, a divisor of the row's bytes and of its address,
+// so no load straddles the row's end.
+template <int U>
+__device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t piece,
+                                            uint32_t (*w)[8]) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int64_t r = row0 + (threadIdx.x & 31) + 32 * q;
-    const unsigned char* p = s + r * nb + kt * SB;
-    const int64_t left = r < rows ? nb - kt * SB : 0;
+    const unsigned char* p = s + r * nb + piece * 32;
+    const int64_t left = r < rows ? nb - piece * 32 : 0;
 #pragma unroll
-    for (int j = 0; j < A; ++j) w[q][j] = 0;
+    for (int j = 0; j < 8; ++j) w[q][j] = 0;
 #pragma unroll
-    for (int i = 0; i < SB / U; ++i) {
+    for (int i = 0; i < 32 / U; ++i) {
       if (i * U < left) {
-        if constexpr (U == 16) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-          w[q][0] = v.x, w[q][A > 1 ? 1 : 0] = v.y, w[q][A > 2 ? 2 : 0] = v.z, w[q][A > 3 ? 3 : 0] = v.w;
-        } else if constexpr (U == 8) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + i);
-          w[q][2 * i] = v.x, w[q][A > 1 ? 2 * i + 1 : 0] = v.y;
+        if constexpr (U == 32) {
+          asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+              : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3]), "=r"(w[q][4]), "=r"(w[q][5]), "=r"(w[q][6]),
+                "=r"(w[q][7])
+              : "l"(p));
+        } else if constexpr (U == 16) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          w[q][4 * i] = v.x, w[q][4 * i + 1] = v.y, w[q][4 * i + 2] = v.z, w[q][4 * i + 3] = v.w;
         } else if constexpr (U == 4) {
           w[q][i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
         } else if constexpr (U == 2) {
@@ -212,10 +214,19 @@ __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0
 
 // Bounded wait for a ring barrier, by the clock alone: the header's flags may
 // still hold what the workspace held before this launch.
+__device__ __forceinline__ bool mm_try_wait(uint64_t* bar, unsigned parity) {  // arrivals may come from the cluster
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned* flags) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mm_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!mm_try_wait(bar, parity)) {
     if (global_ns() - t0 > kWaitLimitNs) {
       atomicOr(flags, kFlagTimeout);
       return false;
@@ -224,51 +235,77 @@ __device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned
   return true;
 }
 
-// A warp brings one 128-row block's scales of the K tiles k0 .. k0 + n - 1 into
-// the ring, kAhead tiles ahead in registers.
-constexpr int kAhead = 4;
-template <int FMT, int U>
-__device__ __forceinline__ void scale_loop(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t k0, int n,
-                                           unsigned char* ring, int stage_bytes, int stages, int atom_bytes,
-                                           uint64_t* full, uint64_t* empty, unsigned* flags) {
-  constexpr int A = TcFormat<FMT>::kAtoms;
-  const int lane = threadIdx.x & 31;
-  uint32_t w[kAhead][4][A];
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u)
-    if (u < n) load_scales<FMT, U>(s, row0, rows, nb, k0 + u, w[u]);
+// A place in the ring, kept by every role over all tiles of a CTA.
+struct MmSlot {
   int slot = 0;
-  unsigned phase = 1;
+  unsigned phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++slot == stages) slot = 0, phase ^= 1;
+  }
+};
+
+// A warp brings one 128-row block's scales of the K tiles k0 .. k0 + n - 1 into
+// the ring.  It reads 32 bytes of a row at a time, the scales of 2, 4 or 8 K
+// tiles (a 16-, 8- or 4-byte read each K tile would move the same 32-byte
+// sector from L2 every time), and the next piece while it writes this one.
+// PAIR: the arrival goes to the pair's even CTA.
+template <int FMT, bool PAIR, int U>
+__device__ __forceinline__ bool scale_loop(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t k0, int n,
+                                           unsigned char* ring, int stage_bytes, int stages, int block_bytes, uint64_t* full,
+                                           uint64_t* empty, unsigned* flags, MmSlot& at) {
+  constexpr int A = TcFormat<FMT>::kAtoms, C = 8 / A;
+  const int lane = threadIdx.x & 31;
+  uint32_t w[4][8], next[4][8];
+  const int64_t last = (k0 + n - 1) / C;
+  load_scales<U>(s, row0, rows, nb, k0 / C, next);
 #pragma unroll 1
-  for (int base = 0; base < n; base += kAhead) {
+  for (int64_t piece = k0 / C; piece <= last; ++piece) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int it = base + u;
-      if (it < n) {
-        if (!__all_sync(0xffffffffu, mm_wait(&empty[slot], phase, flags))) return;
-        unsigned char* dst = ring + slot * stage_bytes + lane * 16;
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[q][j] = next[q][j];
+    if (piece < last) load_scales<U>(s, row0, rows, nb, piece + 1, next);
+#pragma unroll
+    for (int u = 0; u < C; ++u) {
+      const int64_t kt = piece * C + u;
+      if (kt >= k0 && kt < k0 + n) {
+        if (!__all_sync(0xffffffffu, mm_wait(&empty[at.slot], at.phase ^ 1, flags))) return false;
+        unsigned char* dst = ring + at.slot * stage_bytes + lane * 16;
 #pragma unroll
         for (int j = 0; j < A; ++j)
-          *reinterpret_cast<uint4*>(dst + j * atom_bytes) = make_uint4(w[u][0][j], w[u][1][j], w[u][2][j], w[u][3][j]);
+          *reinterpret_cast<uint4*>(dst + j * block_bytes) =
+              make_uint4(w[0][u * A + j], w[1][u * A + j], w[2][u * A + j], w[3][u * A + j]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[slot]);
-        if (it + kAhead < n) load_scales<FMT, U>(s, row0, rows, nb, k0 + it + kAhead, w[u]);
-        if (++slot == stages) slot = 0, phase ^= 1;
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(&full[at.slot], 0);
+          else
+            mbar_arrive(&full[at.slot]);
+        }
+        at.next(stages);
       }
     }
   }
+  return true;
 }
-template <int FMT, typename... Args>
-__device__ __forceinline__ void scale_warp(int unit, Args... args) {
-  if (unit >= TcFormat<FMT>::kScaleBytes)
-    scale_loop<FMT, TcFormat<FMT>::kScaleBytes>(args...);
-  else if (unit >= 4)
-    scale_loop<FMT, 4>(args...);
-  else if (unit == 2)
-    scale_loop<FMT, 2>(args...);
-  else
-    scale_loop<FMT, 1>(args...);
+// `unit`: the largest power of two (32 at most) that divides the scales' address
+// and the row.
+template <int FMT, bool PAIR>
+__device__ __forceinline__ bool scale_warp(int unit, const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t k0,
+                                           int n, unsigned char* ring, int stage_bytes, int stages, int block_bytes,
+                                           uint64_t* full, uint64_t* empty, unsigned* flags, MmSlot& at) {
+#define DQ_SCALE_LOOP(U) \
+  scale_loop<FMT, PAIR, U>(s, row0, rows, nb, k0, n, ring, stage_bytes, stages, block_bytes, full, empty, flags, at)
+  switch (unit) {
+    case 32: return DQ_SCALE_LOOP(32);
+    case 16: return DQ_SCALE_LOOP(16);
+    case 8:
+    case 4: return DQ_SCALE_LOOP(4);
+    case 2: return DQ_SCALE_LOOP(2);
+    default: return DQ_SCALE_LOOP(1);
+  }
+#undef DQ_SCALE_LOOP
 }
 
 struct MmLaunch {
@@ -305,7 +342,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     mbar_fence_init();
     if (blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   }
-  if (warp == 1) tc_alloc<G::kAlloc>(smem_u32(&tmem_base));
+  if (warp == 1) tc_alloc<1, G::kAlloc>(smem_u32(&tmem_base));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -338,28 +375,31 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         const uint32_t sfa = st + G::kA + G::kB, sfb = sfa + G::kSfA;
 #pragma unroll
         for (int j = 0; j < F::kAtoms; ++j) {
-          tc_copy_scales(tmem + G::kSfACol + 4 * j, tc_desc_scales(sfa + 512 * j));
+          tc_copy_scales<1>(tmem + G::kSfACol + 4 * j, tc_desc_scales(sfa + 512 * j));
 #pragma unroll
           for (int h = 0; h < G::kHalves; ++h)
-            tc_copy_scales(tmem + G::kSfBCol + 4 * (j * G::kHalves + h), tc_desc_scales(sfb + 512 * (j * G::kHalves + h)));
+            tc_copy_scales<1>(tmem + G::kSfBCol + 4 * (j * G::kHalves + h), tc_desc_scales(sfb + 512 * (j * G::kHalves + h)));
         }
         const uint64_t da = tc_desc_sw128(st), db = tc_desc_sw128(st + G::kA);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          tc_mma<FMT>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(128, BN, F::byte(k)), tmem + G::kSfACol + 4 * F::atom(k),
+          tc_mma<FMT, 1>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(128, BN, F::byte(k)), tmem + G::kSfACol + 4 * F::atom(k),
                       tmem + G::kSfBCol + 4 * G::kHalves * F::atom(k), it > 0 || k > 0);
-        tc_commit(&empty[slot]);
+        tc_commit<1>(&empty[slot]);
         if (++slot == l.stages) slot = 0, phase ^= 1;
       }
-      tc_commit(&acc_full);
+      tc_commit<1>(&acc_full);
     }
   } else if (warp == 2) {
-    scale_warp<FMT>(l.unit_w, p.ws, n0, p.N, p.K / F::kGroup, k0, n, ring + G::kA + G::kB, G::kStage, l.stages, 512,
-                    full_s, empty, flags);
+    MmSlot at;
+    scale_warp<FMT, false>(l.unit_w, p.ws, n0, p.N, p.K / F::kGroup, k0, n, ring + G::kA + G::kB, G::kStage, l.stages, 512,
+                           full_s, empty, flags, at);
   } else if (warp - 3 < G::kHalves) {
     const int h = warp - 3;
-    scale_warp<FMT>(l.unit_x, p.xs, t0 + 128 * h, p.T, p.K / F::kGroup, k0, n,
-                    ring + G::kA + G::kB + G::kSfA + 512 * h, G::kStage, l.stages, 512 * G::kHalves, full_s, empty, flags);
+    MmSlot at;
+    scale_warp<FMT, false>(l.unit_x, p.xs, t0 + 128 * h, p.T, p.K / F::kGroup, k0, n,
+                           ring + G::kA + G::kB + G::kSfA + 512 * h, G::kStage, l.stages, 512 * G::kHalves, full_s, empty,
+                           flags, at);
   }
   __syncwarp();
 
@@ -378,7 +418,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     for (int c = 0; c < tv && ok; c += 16) {
       uint32_t v[16];
       tc_load16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
-      tc_load_wait();
+      tc_load_wait16(v);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (c + i < tv) {
@@ -394,12 +434,21 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   if (l.split > 1) {
     cluster_sync();
     const uint32_t part = smem_u32(ring);
-    const int total = tv * 128;
+    const int total = tv * 32;  // groups of four features
     for (int e = (int)rank * kMmThreads + threadIdx.x; e < total; e += l.split * kMmThreads) {
-      float s = 0.f;
-      for (int r = 0; r < l.split; ++r) s += ld_cluster_f32(part + 4 * e, r);
-      const int64_t nn = n0 + (e & 127);
-      if (nn < p.N) y_store(p.y, p.y_dt, (t0 + (e >> 7)) * p.N + nn, s * f1 * f2);
+      float4 v[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < l.split) v[r] = ld_cluster_f4(part + 16 * e, r);
+      float4 s = v[0];
+#pragma unroll
+      for (int r = 1; r < 8; ++r)
+        if (r < l.split) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
+      const int64_t nn = n0 + 4 * (e & 31), at = (t0 + (e >> 5)) * p.N + nn;
+      const float o[4] = {s.x * f1 * f2, s.y * f1 * f2, s.z * f1 * f2, s.w * f1 * f2};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (nn + i < p.N) y_store(p.y, p.y_dt, at + i, o[i]);
     }
     cluster_sync();
   } else {
@@ -407,7 +456,258 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   }
   if (warp == 1) {
     tc_fence_after();
-    tc_dealloc<G::kAlloc>(tmem);
+    tc_dealloc<1, G::kAlloc>(tmem);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tensor-core product of many tokens: pairs of CTAs (tcgen05 cta_group::2)
+// compute tiles of 256 tokens x 256 features, persistently.  Each CTA of a
+// pair holds 128 tokens and 128 features of a K tile, and the tensor cores of
+// both read both halves of the features: half the shared-memory fill per
+// multiply-add of a single CTA's 128 x 256 tile, which the L2's bandwidth
+// would bound.  The even CTA issues the multiply-adds; copies and scale warps
+// of both signal its barriers.
+//
+// Warps: 0 .. 7 write tiles out (lane quarter w % 4, column half w / 4), 8
+// issues the copies, 9 the tensor-core work, 10 brings the tokens' scales, 11
+// and 12 the features'.  A finished tile is read into registers, rounded to
+// the output type and released before it is stored, so the next tile's
+// multiply-adds wait for the tensor-memory reads alone.
+constexpr int kPairThreads = 13 * 32;
+constexpr int kPairEpilogue = 8;  // warps
+constexpr int kPairStages = 5;
+
+template <int FMT>
+struct PairGeo {
+  using F = TcFormat<FMT>;
+  static constexpr int kA = 128 * 128, kB = 128 * 128;
+  static constexpr int kSfA = F::kAtoms * 512, kSfB = F::kAtoms * 1024;
+  static constexpr int kStage = (kA + kB + kSfA + kSfB + 1023) / 1024 * 1024;
+  static constexpr int kTurn = kPairEpilogue * 32 * 33 * 4;  // a padded 32 x 32 block per epilogue warp
+  static constexpr int kSmem = kPairStages * kStage + kTurn + 1024;
+  static constexpr int kScaleCols = 16 + 32;  // tensor-memory columns of one set of scales; two sets take turns
+};
+
+struct PairLaunch {
+  int64_t tiles_m, tiles_n, tiles;
+  int unit_x, unit_w;
+  int wide;  // rows of Y start at multiples of 32 bytes
+};
+
+// Tile order: bands of 8 token tiles, features within, so that the pairs at
+// work at one time share operands in L2.
+__device__ __forceinline__ void pair_tile(const PairLaunch& l, int64_t i, int64_t& m, int64_t& n) {
+  const int64_t band = i / (8 * l.tiles_n), rest = i - band * 8 * l.tiles_n;
+  const int64_t height = min((int64_t)8, l.tiles_m - band * 8);
+  m = band * 8 + rest % height;
+  n = rest / height;
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dt) {
+  uint32_t r;
+  if (dt == DT_BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Stores 32 rows x 32 columns of a warp, lane = row, v[c] = column c (16-bit
+// outputs: two columns a word), where rows of Y have no useful alignment:
+// through the warp's padded block of shared memory, so that lanes write
+// neighbouring columns.
+template <bool OUT32>
+__device__ __forceinline__ void store_turned(const MatmulProblem& p, float* turn, const uint32_t* v, int64_t t, int64_t n) {
+  const int lane = threadIdx.x & 31;
+  uint32_t* b = reinterpret_cast<uint32_t*>(turn);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    b[lane * 33 + c] = OUT32 ? v[c] : ((c & 1) ? v[c / 2] >> 16 : v[c / 2] & 0xFFFFu);
+  __syncwarp();
+  const int rows = (int)max((int64_t)0, min((int64_t)32, p.T - t));
+  if (n + lane < p.N)
+    for (int r = 0; r < rows; ++r) {
+      const int64_t at = (t + r) * p.N + n + lane;
+      if (OUT32)
+        reinterpret_cast<uint32_t*>(p.y)[at] = b[r * 33 + lane];
+      else
+        reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)b[r * 33 + lane];
+    }
+}
+
+template <int FMT, bool OUT32>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_matmul_pair(MatmulProblem p, PairLaunch l, const __grid_constant__ CUtensorMap wmap,
+                  const __grid_constant__ CUtensorMap xmap) {
+  using G = PairGeo<FMT>;
+  using F = TcFormat<FMT>;
+  extern __shared__ unsigned char mm_smem[];
+  __shared__ uint64_t full_t[kPairStages], full_s[kPairStages], empty[kPairStages], acc_full, acc_empty;
+  __shared__ uint32_t tmem_base;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int nk = (int)((p.K + F::kTileK - 1) / F::kTileK);
+  const int64_t nb = p.K / F::kGroup;
+  unsigned* flags = &p.hdr->flags;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&full_t[i], 1);
+      mbar_init(&full_s[i], 2 * 3);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&acc_full, 1);
+    mbar_init(&acc_empty, 2 * kPairEpilogue);
+    mbar_fence_init();
+    if (blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
+  }
+  if (warp == 9) tc_alloc<2, 512>(smem_u32(&tmem_base));
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  MmSlot at;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      bool ok = true;
+      int64_t issued = 0;
+      for (int64_t i = pair; i < l.tiles && ok; i += pairs) {
+        int64_t m, n;
+        pair_tile(l, i, m, n);
+        for (int kt = 0; kt < nk; ++kt, ++issued) {
+          if (!(ok = mm_wait(&empty[at.slot], at.phase ^ 1, flags))) break;
+          unsigned char* st = ring + at.slot * G::kStage;
+          if (rank == 0) mbar_arrive_expect_tx(&full_t[at.slot], 2 * (G::kA + G::kB));
+          tma_load_2d_pair(st, &xmap, kt * 128, (int)(m * 256 + rank * 128), &full_t[at.slot]);
+          tma_load_2d_pair(st + G::kA, &wmap, kt * 128, (int)(n * 256 + rank * 128), &full_t[at.slot]);
+          at.next(kPairStages);
+        }
+      }
+      if (!ok && rank == 0)  // both CTAs' copies land before the pair leaves
+        for (int64_t i = max((int64_t)0, issued - kPairStages); i < issued; ++i)
+          mbar_drain(&full_t[i % kPairStages], (unsigned)(i / kPairStages) & 1);
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && rank == 0) {
+      unsigned turn = 0, set = 0;
+      bool ok = true;
+      for (int64_t i = pair; i < l.tiles && ok; i += pairs, turn ^= 1) {
+        if (!(ok = mm_wait(&acc_empty, turn ^ 1, flags))) break;
+        tc_fence_after();
+        for (int kt = 0; kt < nk; ++kt, set ^= 1) {
+          if (!(ok = mm_wait(&full_s[at.slot], at.phase, flags) && mm_wait(&full_t[at.slot], at.phase, flags))) break;
+          tc_fence_after();
+          const uint32_t st = smem_u32(ring + at.slot * G::kStage);
+          const uint32_t sa = st + G::kA + G::kB, sb = sa + G::kSfA;
+          const uint32_t ca = tmem + 256 + set * G::kScaleCols, cb = ca + 16;
+#pragma unroll
+          for (int j = 0; j < F::kAtoms; ++j) {
+            tc_copy_scales<2>(ca + 4 * j, tc_desc_scales(sa + 512 * j));
+            tc_copy_scales<2>(cb + 8 * j, tc_desc_scales(sb + 1024 * j));
+            tc_copy_scales<2>(cb + 8 * j + 4, tc_desc_scales(sb + 1024 * j + 512));
+          }
+          const uint64_t da = tc_desc_sw128(st), db = tc_desc_sw128(st + G::kA);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma<FMT, 2>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(256, 256, F::byte(k)), ca + 4 * F::atom(k),
+                           cb + 8 * F::atom(k), kt > 0 || k > 0);
+          tc_commit<2>(&empty[at.slot]);
+          at.next(kPairStages);
+        }
+        tc_commit<2>(&acc_full);
+      }
+    }
+  } else if (warp >= 10) {
+    bool ok = true;
+    for (int64_t i = pair; i < l.tiles && ok; i += pairs) {
+      int64_t m, n;
+      pair_tile(l, i, m, n);
+      if (warp == 10)
+        ok = scale_warp<FMT, true>(l.unit_x, p.xs, m * 256 + rank * 128, p.T, nb, (int64_t)0, nk, ring + G::kA + G::kB,
+                                   G::kStage, kPairStages, 512, full_s, empty, flags, at);
+      else
+        ok = scale_warp<FMT, true>(l.unit_w, p.ws, n * 256 + (warp - 11) * 128, p.N, nb, (int64_t)0, nk,
+                                   ring + G::kA + G::kB + G::kSfA + (warp - 11) * 512, G::kStage, kPairStages, 1024, full_s,
+                                   empty, flags, at);
+    }
+  } else {
+    float f1, f2;
+    tensor_factors(p, f1, f2);
+    const int q = warp & 3, half = warp >> 2;
+    float* turned = reinterpret_cast<float*>(ring + kPairStages * G::kStage) + warp * 32 * 33;
+    unsigned turn = 0;
+    for (int64_t i = pair; i < l.tiles; i += pairs, turn ^= 1) {
+      int64_t m, n;
+      pair_tile(l, i, m, n);
+      if (!__all_sync(0xffffffffu, mm_wait(&acc_full, turn, flags))) break;
+      tc_fence_after();
+      const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
+      const int64_t t0 = m * 256 + rank * 128 + 32 * q, t = t0 + lane, nn = n * 256 + 128 * half;
+      if (!OUT32) {
+        uint32_t o[64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tc_load32(src + 32 * c, v);
+          tc_load_wait32(v);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[16 * c + e] = pack16(__uint_as_float(v[2 * e]) * f1 * f2, __uint_as_float(v[2 * e + 1]) * f1 * f2, p.y_dt);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(&acc_empty, 0);
+        if (l.wide) {
+          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + t * p.N + nn;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (t < p.T && nn + 16 * c < p.N) st_global_32b(y + 16 * c, o + 8 * c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) store_turned<false>(p, turned, o + 16 * c, t0, nn + 32 * c);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[32];
+          tc_load32(src + 32 * c, v);
+          tc_load_wait32(v);
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(&acc_empty, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f1 * f2);
+          if (l.wide) {
+            uint32_t* y = reinterpret_cast<uint32_t*>(p.y) + t * p.N + nn + 32 * c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (t < p.T && nn + 32 * c + 8 * e < p.N) st_global_32b(y + 8 * e, v + 8 * e);
+          } else {
+            store_turned<true>(p, turned, v, t0, nn + 32 * c);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may still signal it or read its shared memory
+  if (warp == 9) {
+    tc_fence_after();
+    tc_dealloc<2, 512>(tmem);
   }
 }
 
@@ -433,7 +733,7 @@ static bool encode_codes(CUtensorMap* map, const unsigned char* q, int64_t row_b
 }
 
 static int scale_unit(const unsigned char* s, int64_t nb) {
-  const uintptr_t v = (uintptr_t)s | (uintptr_t)nb | 16u;
+  const uintptr_t v = (uintptr_t)s | (uintptr_t)nb | 32u;
   return (int)(v & (~v + 1));
 }
 
@@ -477,6 +777,39 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, p, l, wmap, xmap);
 }
 
+template <int FMT, bool OUT32>
+static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st) {
+  using G = PairGeo<FMT>;
+  CUtensorMap wmap, xmap;
+  const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
+  if (!encode_codes(&wmap, p.wq, row_bytes, p.N, 128) || !encode_codes(&xmap, p.xq, row_bytes, p.T, 128))
+    return cudaErrorInvalidValue;
+  PairLaunch l;
+  l.tiles_m = (p.T + 255) / 256;
+  l.tiles_n = (p.N + 255) / 256;
+  l.tiles = l.tiles_m * l.tiles_n;
+  l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
+  l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
+  l.wide = ((uintptr_t)p.y | (uintptr_t)(p.N * (OUT32 ? 4 : 2))) % 32 == 0;
+  auto kern = k_matmul_pair<FMT, OUT32>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = l.tiles < sms / 2 ? l.tiles : sms / 2;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = (size_t)G::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, l, wmap, xmap);
+}
+
 template <int FMT>
 static cudaError_t matmul_fmt(const MatmulProblem& p, int sms, cudaStream_t st) {
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
@@ -484,8 +817,8 @@ static cudaError_t matmul_fmt(const MatmulProblem& p, int sms, cudaStream_t st) 
   if (p.T <= 16) return matmul_tc<FMT, 16>(p, sms, st);
   if (p.T <= 32) return matmul_tc<FMT, 32>(p, sms, st);
   if (p.T <= 64) return matmul_tc<FMT, 64>(p, sms, st);
-  if (p.T <= 128 || (p.N + 127) / 128 * ((p.T + 255) / 256) < sms) return matmul_tc<FMT, 128>(p, sms, st);
-  return matmul_tc<FMT, 256>(p, sms, st);
+  if (p.T <= 128 || (p.N + 255) / 256 * ((p.T + 255) / 256) < sms / 4) return matmul_tc<FMT, 128>(p, sms, st);
+  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, sms, st) : matmul_pair<FMT, false>(p, sms, st);
 }
 
 }  // namespace dq
