@@ -157,21 +157,22 @@ static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
 // distributed shared memory in rank order (no atomics: equal calls give equal
 // bits).
 //
-// Warps: 0 issues the copies, 1 the tensor-core work; 2 .. 4 bring scales and,
-// with 5, write the tile out (warp w reads tensor-memory lanes 32 (w % 4) ..).
+// Warps: 0 issues the copies, 1 the tensor-core work; 2 and 4 bring the
+// weights' scales, 3 and 5 the tokens', and the four write the tile out (warp w
+// reads tensor-memory lanes 32 (w % 4) ..).
 constexpr int kMmThreads = 192;
 constexpr int kMmMaxStages = 8;
 
 template <int FMT, int BN>
 struct MmGeo {
   using F = TcFormat<FMT>;
-  static constexpr int kHalves = (BN + 127) / 128;  // 128-row blocks of the token scales
+  static_assert(BN <= 128, "one 128-row block of token scales");
   static constexpr int kA = 128 * 128, kB = BN * 128;
-  static constexpr int kSfA = F::kAtoms * 512, kSfB = F::kAtoms * 512 * kHalves;
+  static constexpr int kSfA = F::kAtoms * 512, kSfB = F::kAtoms * 512;
   static constexpr int kStage = (kA + kB + kSfA + kSfB + 1023) / 1024 * 1024;
   static constexpr int kAccCols = BN < 32 ? 32 : BN;
   static constexpr int kSfACol = kAccCols, kSfBCol = kAccCols + 16;
-  static constexpr int kCols = kAccCols + 16 + 16 * kHalves;
+  static constexpr int kCols = kAccCols + 16 + 16;
   static constexpr int kAlloc = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
 };
 
@@ -212,21 +213,20 @@ __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0
   }
 }
 
+// The same out of line for scales at odd addresses (1- and 2-byte loads, up to
+// 128 a lane): inlined, they took the registers of the paths that matter.
+template <int U>
+static __device__ __noinline__ void load_scales_far(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb,
+                                                    int64_t piece, uint32_t (*w)[8]) {
+  load_scales<U>(s, row0, rows, nb, piece, w);
+}
+
 // Bounded wait for a ring barrier, by the clock alone: the header's flags may
 // still hold what the workspace held before this launch.
-__device__ __forceinline__ bool mm_try_wait(uint64_t* bar, unsigned parity) {  // arrivals may come from the cluster
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned* flags) {
-  if (mm_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = global_ns();
-  while (!mm_try_wait(bar, parity)) {
+  while (!mbar_try_wait(bar, parity)) {
     if (global_ns() - t0 > kWaitLimitNs) {
       atomicOr(flags, kFlagTimeout);
       return false;
@@ -244,59 +244,78 @@ struct MmSlot {
   }
 };
 
-// A warp brings one 128-row block's scales of the K tiles k0 .. k0 + n - 1 into
-// the ring.  It reads 32 bytes of a row at a time, the scales of 2, 4 or 8 K
-// tiles (a 16-, 8- or 4-byte read each K tile would move the same 32-byte
-// sector from L2 every time), and the next piece while it writes this one.
+// What a scale warp keeps over all its tiles.  `pass`: two barriers of the
+// block's two warps, on which warp t says that it has written its piece.
+struct ScaleTurn {
+  uint64_t* pass;
+  int turn;             // 0 or 1
+  unsigned piece = 0;   // pieces of the block so far
+  MmSlot at;
+};
+
+// Two warps bring one 128-row block's scales of the K tiles k0 .. k0 + n - 1
+// into the ring.  A warp reads 32 bytes of a row at a time, the scales of 2, 4
+// or 8 K tiles (a 16-, 8- or 4-byte read each K tile would move the same
+// 32-byte sector from L2 every time); the two take turns, because the proxy
+// fence that publishes a K tile waits for the warp's own reads in flight: one
+// warp reading ahead took about 1700 clocks a K tile.  A warp writes its piece
+// only after the other has written the one before: a ring barrier's phase is
+// known by its parity alone, so every slot must be waited for in order.
 // PAIR: the arrival goes to the pair's even CTA.
 template <int FMT, bool PAIR, int U>
-__device__ __forceinline__ bool scale_loop(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t k0, int n,
-                                           unsigned char* ring, int stage_bytes, int stages, int block_bytes, uint64_t* full,
-                                           uint64_t* empty, unsigned* flags, MmSlot& at) {
+__device__ __forceinline__ bool scale_loop(ScaleTurn& t, const unsigned char* s, int64_t row0, int64_t rows, int64_t nb,
+                                           int64_t k0, int n, unsigned char* ring, int stage_bytes, int stages,
+                                           int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags) {
   constexpr int A = TcFormat<FMT>::kAtoms, C = 8 / A;
   const int lane = threadIdx.x & 31;
-  uint32_t w[4][8], next[4][8];
   const int64_t last = (k0 + n - 1) / C;
-  load_scales<U>(s, row0, rows, nb, k0 / C, next);
 #pragma unroll 1
-  for (int64_t piece = k0 / C; piece <= last; ++piece) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[q][j] = next[q][j];
-    if (piece < last) load_scales<U>(s, row0, rows, nb, piece + 1, next);
+  for (int64_t piece = k0 / C; piece <= last; ++piece, ++t.piece) {
+    const bool mine = (int)(t.piece & 1) == t.turn;
+    uint32_t w[4][8];
+    if (mine) {
+      if constexpr (U >= 4)
+        load_scales<U>(s, row0, rows, nb, piece, w);
+      else
+        load_scales_far<U>(s, row0, rows, nb, piece, w);
+      // the other warp's piece before this one: its (piece - 1) / 2-th
+      if (t.piece > 0 && !__all_sync(0xffffffffu, mm_wait(&t.pass[t.turn ^ 1], ((t.piece - 1) >> 1) & 1, flags))) return false;
+    }
 #pragma unroll
     for (int u = 0; u < C; ++u) {
       const int64_t kt = piece * C + u;
       if (kt >= k0 && kt < k0 + n) {
-        if (!__all_sync(0xffffffffu, mm_wait(&empty[at.slot], at.phase ^ 1, flags))) return false;
-        unsigned char* dst = ring + at.slot * stage_bytes + lane * 16;
+        if (mine) {
+          if (!__all_sync(0xffffffffu, mm_wait(&empty[t.at.slot], t.at.phase ^ 1, flags))) return false;
+          unsigned char* dst = ring + t.at.slot * stage_bytes + lane * 16;
 #pragma unroll
-        for (int j = 0; j < A; ++j)
-          *reinterpret_cast<uint4*>(dst + j * block_bytes) =
-              make_uint4(w[0][u * A + j], w[1][u * A + j], w[2][u * A + j], w[3][u * A + j]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR)
-            mbar_arrive_cluster(&full[at.slot], 0);
-          else
-            mbar_arrive(&full[at.slot]);
+          for (int j = 0; j < A; ++j)
+            *reinterpret_cast<uint4*>(dst + j * block_bytes) =
+                make_uint4(w[0][u * A + j], w[1][u * A + j], w[2][u * A + j], w[3][u * A + j]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (PAIR)
+              mbar_arrive_cluster(&full[t.at.slot], 0);
+            else
+              mbar_arrive(&full[t.at.slot]);
+          }
         }
-        at.next(stages);
+        t.at.next(stages);
       }
     }
+    if (mine && lane == 0) mbar_arrive(&t.pass[t.turn]);
   }
   return true;
 }
 // `unit`: the largest power of two (32 at most) that divides the scales' address
 // and the row.
 template <int FMT, bool PAIR>
-__device__ __forceinline__ bool scale_warp(int unit, const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t k0,
-                                           int n, unsigned char* ring, int stage_bytes, int stages, int block_bytes,
-                                           uint64_t* full, uint64_t* empty, unsigned* flags, MmSlot& at) {
+__device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, const unsigned char* s, int64_t row0, int64_t rows, int64_t nb,
+                                           int64_t k0, int n, unsigned char* ring, int stage_bytes, int stages, int block_bytes,
+                                           uint64_t* full, uint64_t* empty, unsigned* flags) {
 #define DQ_SCALE_LOOP(U) \
-  scale_loop<FMT, PAIR, U>(s, row0, rows, nb, k0, n, ring, stage_bytes, stages, block_bytes, full, empty, flags, at)
+  scale_loop<FMT, PAIR, U>(t, s, row0, rows, nb, k0, n, ring, stage_bytes, stages, block_bytes, full, empty, flags)
   switch (unit) {
     case 32: return DQ_SCALE_LOOP(32);
     case 16: return DQ_SCALE_LOOP(16);
@@ -320,10 +339,10 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   using G = MmGeo<FMT, BN>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kMmMaxStages], full_s[kMmMaxStages], empty[kMmMaxStages], acc_full;
+  __shared__ uint64_t full_t[kMmMaxStages], full_s[kMmMaxStages], empty[kMmMaxStages], pass[4], acc_full;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int64_t tiles_n = (p.N + 127) / 128;
   const int64_t tile = blockIdx.x / l.split;
   const uint32_t rank = blockIdx.x % l.split;
@@ -335,9 +354,10 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < l.stages; ++i) {
       mbar_init(&full_t[i], 1);
-      mbar_init(&full_s[i], 1 + G::kHalves);
+      mbar_init(&full_s[i], 2);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&pass[i], 1);
     mbar_init(&acc_full, 1);
     mbar_fence_init();
     if (blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
@@ -349,7 +369,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   const uint32_t tmem = tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int slot = 0, issued = 0;
       unsigned phase = 1;
       bool ok = true;
@@ -365,7 +385,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         for (int i = max(0, issued - l.stages); i < issued; ++i) mbar_drain(&full_t[i % l.stages], (i / l.stages) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       int slot = 0;
       unsigned phase = 0;
       for (int it = 0; it < n; ++it) {
@@ -376,30 +396,24 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 #pragma unroll
         for (int j = 0; j < F::kAtoms; ++j) {
           tc_copy_scales<1>(tmem + G::kSfACol + 4 * j, tc_desc_scales(sfa + 512 * j));
-#pragma unroll
-          for (int h = 0; h < G::kHalves; ++h)
-            tc_copy_scales<1>(tmem + G::kSfBCol + 4 * (j * G::kHalves + h), tc_desc_scales(sfb + 512 * (j * G::kHalves + h)));
+          tc_copy_scales<1>(tmem + G::kSfBCol + 4 * j, tc_desc_scales(sfb + 512 * j));
         }
         const uint64_t da = tc_desc_sw128(st), db = tc_desc_sw128(st + G::kA);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           tc_mma<FMT, 1>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(128, BN, F::byte(k)), tmem + G::kSfACol + 4 * F::atom(k),
-                      tmem + G::kSfBCol + 4 * G::kHalves * F::atom(k), it > 0 || k > 0);
+                      tmem + G::kSfBCol + 4 * F::atom(k), it > 0 || k > 0);
         tc_commit<1>(&empty[slot]);
         if (++slot == l.stages) slot = 0, phase ^= 1;
       }
       tc_commit<1>(&acc_full);
     }
-  } else if (warp == 2) {
-    MmSlot at;
-    scale_warp<FMT, false>(l.unit_w, p.ws, n0, p.N, p.K / F::kGroup, k0, n, ring + G::kA + G::kB, G::kStage, l.stages, 512,
-                           full_s, empty, flags, at);
-  } else if (warp - 3 < G::kHalves) {
-    const int h = warp - 3;
-    MmSlot at;
-    scale_warp<FMT, false>(l.unit_x, p.xs, t0 + 128 * h, p.T, p.K / F::kGroup, k0, n,
-                           ring + G::kA + G::kB + G::kSfA + 512 * h, G::kStage, l.stages, 512 * G::kHalves, full_s, empty,
-                           flags, at);
+  } else {
+    const bool of_w = (warp & 1) == 0;
+    ScaleTurn t{&pass[of_w ? 0 : 2], (warp - 2) >> 1};
+    scale_warp<FMT, false>(of_w ? l.unit_w : l.unit_x, t, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
+                           p.K / F::kGroup, k0, n, ring + G::kA + G::kB + (of_w ? 0 : G::kSfA), G::kStage, l.stages, 512,
+                           full_s, empty, flags);
   }
   __syncwarp();
 
@@ -470,11 +484,11 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 // of both signal its barriers.
 //
 // Warps: 0 .. 7 write tiles out (lane quarter w % 4, column half w / 4), 8
-// issues the copies, 9 the tensor-core work, 10 brings the tokens' scales, 11
-// and 12 the features'.  A finished tile is read into registers, rounded to
+// issues the copies, 9 the tensor-core work, 10 and 11 bring the tokens' scales,
+// 12 .. 15 the features' (two warps a 128-row block).  A finished tile is read into registers, rounded to
 // the output type and released before it is stored, so the next tile's
 // multiply-adds wait for the tensor-memory reads alone.
-constexpr int kPairThreads = 13 * 32;
+constexpr int kPairThreads = 16 * 32;
 constexpr int kPairEpilogue = 8;  // warps
 constexpr int kPairStages = 5;
 
@@ -550,10 +564,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using G = PairGeo<FMT>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kPairStages], full_s[kPairStages], empty[kPairStages], acc_full, acc_empty;
+  __shared__ uint64_t full_t[kPairStages], full_s[kPairStages], empty[kPairStages], pass[6], acc_full, acc_empty;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   const int nk = (int)((p.K + F::kTileK - 1) / F::kTileK);
@@ -565,6 +579,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&full_s[i], 2 * 3);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < 6; ++i) mbar_init(&pass[i], 1);
     mbar_init(&acc_full, 1);
     mbar_init(&acc_empty, 2 * kPairEpilogue);
     mbar_fence_init();
@@ -579,7 +594,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   MmSlot at;
 
   if (warp == 8) {
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       int64_t issued = 0;
       for (int64_t i = pair; i < l.tiles && ok; i += pairs) {
@@ -599,7 +614,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           mbar_drain(&full_t[i % kPairStages], (unsigned)(i / kPairStages) & 1);
     }
   } else if (warp == 9) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       unsigned turn = 0, set = 0;
       bool ok = true;
       for (int64_t i = pair; i < l.tiles && ok; i += pairs, turn ^= 1) {
@@ -629,17 +644,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     }
   } else if (warp >= 10) {
+    const int block = (warp - 10) >> 1;  // 0: the tokens, 1 and 2: the features' halves
+    const bool of_x = block == 0;
+    ScaleTurn t{&pass[2 * block], warp & 1};
     bool ok = true;
     for (int64_t i = pair; i < l.tiles && ok; i += pairs) {
       int64_t m, n;
       pair_tile(l, i, m, n);
-      if (warp == 10)
-        ok = scale_warp<FMT, true>(l.unit_x, p.xs, m * 256 + rank * 128, p.T, nb, (int64_t)0, nk, ring + G::kA + G::kB,
-                                   G::kStage, kPairStages, 512, full_s, empty, flags, at);
-      else
-        ok = scale_warp<FMT, true>(l.unit_w, p.ws, n * 256 + (warp - 11) * 128, p.N, nb, (int64_t)0, nk,
-                                   ring + G::kA + G::kB + G::kSfA + (warp - 11) * 512, G::kStage, kPairStages, 1024, full_s,
-                                   empty, flags, at);
+      ok = scale_warp<FMT, true>(of_x ? l.unit_x : l.unit_w, t, of_x ? p.xs : p.ws,
+                                 of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, (int64_t)0,
+                                 nk, ring + G::kA + G::kB + (of_x ? 0 : G::kSfA + (block - 1) * 512), G::kStage, kPairStages,
+                                 of_x ? 512 : 1024, full_s, empty, flags);
     }
   } else {
     float f1, f2;
@@ -760,7 +775,16 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
   smem += 1024;
   auto kern = k_matmul_tc<FMT, BN>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  // A CTA takes at least its tensor memory's share of the SM's shared memory
+  // (228 KB, 1 KB of it per CTA reserved).  Then tensor memory never runs out on
+  // an SM before shared memory does, and no CTA of a cluster can wait for tensor
+  // memory that is held by CTAs which wait for their own cluster.
+  const int share = 228 * 1024 / 512 * G::kAlloc - 1024 - (int)fa.sharedSizeBytes;
+  if (smem < share) smem = share;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
