@@ -129,11 +129,15 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int
       : "memory");
 }
 
-// Arrival on the barrier at this place in the cluster's CTA `rank`.
+// Arrival on the barrier at this place in the cluster's CTA `rank`.  Release at
+// the CTA's scope: what it publishes are writes to this CTA's shared memory, read
+// by this SM's tensor core after a proxy fence, and tensor-memory reads that a
+// tcgen05 fence ordered.  At cluster scope the arrival waited for the warp's
+// memory traffic, about 1500 clocks.
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\n"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar)),
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
 }
