@@ -168,8 +168,8 @@ struct MmGeo {
   using F = TcFormat<FMT>;
   static_assert(BN <= 128, "one 128-row block of token scales");
   static constexpr int kA = 128 * 128, kB = BN * 128;
-  static constexpr int kSfA = F::kAtoms * 512, kSfB = F::kAtoms * 512;
-  static constexpr int kStage = (kA + kB + kSfA + kSfB + 1023) / 1024 * 1024;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kScales = 2 * 4096;  // a slot of the piece ring: 32 bytes of 128 features and of 128 tokens
   static constexpr int kAccCols = BN < 32 ? 32 : BN;
   static constexpr int kSfACol = kAccCols, kSfBCol = kAccCols + 16;
   static constexpr int kCols = kAccCols + 16 + 16;
@@ -244,78 +244,59 @@ struct MmSlot {
   }
 };
 
-// What a scale warp keeps over all its tiles.  `pass`: two barriers of the
-// block's two warps, on which warp t says that it has written its piece.
+// Scales travel in pieces of 32 bytes a row, one memory sector: the scales of
+// 2, 4 or 8 K tiles.  (Read a K tile at a time, the same sector would come from
+// L2 every time, and every K tile would cost its own barriers.)  The piece ring
+// has two slots and each 128-row block two warps that take turns, warp t filling
+// slot t, so that one reads while the other waits or writes: the proxy fence
+// that publishes a piece waits for the warp's own reads in flight.
 struct ScaleTurn {
-  uint64_t* pass;
-  int turn;             // 0 or 1
-  unsigned piece = 0;   // pieces of the block so far
-  MmSlot at;
+  int turn;            // 0 or 1
+  unsigned piece = 0;  // pieces of the block so far, over all its tiles
 };
 
-// Two warps bring one 128-row block's scales of the K tiles k0 .. k0 + n - 1
-// into the ring.  A warp reads 32 bytes of a row at a time, the scales of 2, 4
-// or 8 K tiles (a 16-, 8- or 4-byte read each K tile would move the same
-// 32-byte sector from L2 every time); the two take turns, because the proxy
-// fence that publishes a K tile waits for the warp's own reads in flight: one
-// warp reading ahead took about 1700 clocks a K tile.  A warp writes its piece
-// only after the other has written the one before: a ring barrier's phase is
-// known by its parity alone, so every slot must be waited for in order.
+// A warp's share of one block's scales of the K tiles k0 .. k0 + n - 1.  Slot t
+// of the ring starts at ring + t * slot_bytes; the words of K tile u of a piece
+// and scale word j are the 512-byte block u * kAtoms + j, block_bytes apart.
 // PAIR: the arrival goes to the pair's even CTA.
-template <int FMT, bool PAIR, int U>
-__device__ __forceinline__ bool scale_loop(ScaleTurn& t, const unsigned char* s, int64_t row0, int64_t rows, int64_t nb,
-                                           int64_t k0, int n, unsigned char* ring, int stage_bytes, int stages,
-                                           int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags) {
-  constexpr int A = TcFormat<FMT>::kAtoms, C = 8 / A;
+template <bool PAIR, int U>
+__device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0, int64_t rows,
+                                           int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes, int block_bytes,
+                                           uint64_t* full, uint64_t* empty, unsigned* flags) {
   const int lane = threadIdx.x & 31;
-  const int64_t last = (k0 + n - 1) / C;
+  const int last = (k0 + n - 1) / tiles_per_piece;
 #pragma unroll 1
-  for (int64_t piece = k0 / C; piece <= last; ++piece, ++t.piece) {
-    const bool mine = (int)(t.piece & 1) == t.turn;
+  for (int piece = k0 / tiles_per_piece; piece <= last; ++piece, ++t.piece) {
+    if ((int)(t.piece & 1) != t.turn) continue;
     uint32_t w[4][8];
-    if (mine) {
-      if constexpr (U >= 4)
-        load_scales<U>(s, row0, rows, nb, piece, w);
+    if constexpr (U >= 4)
+      load_scales<U>(s, row0, rows, nb, piece, w);
+    else
+      load_scales_far<U>(s, row0, rows, nb, piece, w);
+    if (!__all_sync(0xffffffffu, mm_wait(&empty[t.turn], ((t.piece >> 1) & 1) ^ 1, flags))) return false;
+    unsigned char* dst = ring + t.turn * slot_bytes + lane * 16;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      *reinterpret_cast<uint4*>(dst + j * block_bytes) = make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (PAIR)
+        mbar_arrive_cluster(&full[t.turn], 0);
       else
-        load_scales_far<U>(s, row0, rows, nb, piece, w);
-      // the other warp's piece before this one: its (piece - 1) / 2-th
-      if (t.piece > 0 && !__all_sync(0xffffffffu, mm_wait(&t.pass[t.turn ^ 1], ((t.piece - 1) >> 1) & 1, flags))) return false;
+        mbar_arrive(&full[t.turn]);
     }
-#pragma unroll
-    for (int u = 0; u < C; ++u) {
-      const int64_t kt = piece * C + u;
-      if (kt >= k0 && kt < k0 + n) {
-        if (mine) {
-          if (!__all_sync(0xffffffffu, mm_wait(&empty[t.at.slot], t.at.phase ^ 1, flags))) return false;
-          unsigned char* dst = ring + t.at.slot * stage_bytes + lane * 16;
-#pragma unroll
-          for (int j = 0; j < A; ++j)
-            *reinterpret_cast<uint4*>(dst + j * block_bytes) =
-                make_uint4(w[0][u * A + j], w[1][u * A + j], w[2][u * A + j], w[3][u * A + j]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (PAIR)
-              mbar_arrive_cluster(&full[t.at.slot], 0);
-            else
-              mbar_arrive(&full[t.at.slot]);
-          }
-        }
-        t.at.next(stages);
-      }
-    }
-    if (mine && lane == 0) mbar_arrive(&t.pass[t.turn]);
   }
   return true;
 }
 // `unit`: the largest power of two (32 at most) that divides the scales' address
 // and the row.
-template <int FMT, bool PAIR>
-__device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, const unsigned char* s, int64_t row0, int64_t rows, int64_t nb,
-                                           int64_t k0, int n, unsigned char* ring, int stage_bytes, int stages, int block_bytes,
-                                           uint64_t* full, uint64_t* empty, unsigned* flags) {
+template <bool PAIR>
+__device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0,
+                                           int64_t rows, int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes,
+                                           int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags) {
 #define DQ_SCALE_LOOP(U) \
-  scale_loop<FMT, PAIR, U>(t, s, row0, rows, nb, k0, n, ring, stage_bytes, stages, block_bytes, full, empty, flags)
+  scale_loop<PAIR, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, flags)
   switch (unit) {
     case 32: return DQ_SCALE_LOOP(32);
     case 16: return DQ_SCALE_LOOP(16);
@@ -339,9 +320,10 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   using G = MmGeo<FMT, BN>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kMmMaxStages], full_s[kMmMaxStages], empty[kMmMaxStages], pass[4], acc_full;
+  __shared__ uint64_t full_t[kMmMaxStages], empty[kMmMaxStages], full_s[2], empty_s[2], acc_full;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
+  unsigned char* scales = ring + l.stages * G::kStage;
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int64_t tiles_n = (p.N + 127) / 128;
   const int64_t tile = blockIdx.x / l.split;
@@ -354,10 +336,12 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   if (threadIdx.x == 0) {
     for (int i = 0; i < l.stages; ++i) {
       mbar_init(&full_t[i], 1);
-      mbar_init(&full_s[i], 2);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&pass[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full_s[i], 2);
+      mbar_init(&empty_s[i], 1);
+    }
     mbar_init(&acc_full, 1);
     mbar_fence_init();
     if (blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
@@ -386,13 +370,15 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      int slot = 0;
-      unsigned phase = 0;
+      MmSlot at;
+      unsigned piece = 0;
       for (int it = 0; it < n; ++it) {
-        if (!mm_wait(&full_s[slot], phase, flags) || !mm_wait(&full_t[slot], phase, flags)) break;
+        const int kt = (int)k0 + it, u = kt % F::kPiece;
+        if ((it == 0 || u == 0) && !mm_wait(&full_s[piece & 1], (piece >> 1) & 1, flags)) break;
+        if (!mm_wait(&full_t[at.slot], at.phase, flags)) break;
         tc_fence_after();
-        const uint32_t st = smem_u32(ring + slot * G::kStage);
-        const uint32_t sfa = st + G::kA + G::kB, sfb = sfa + G::kSfA;
+        const uint32_t st = smem_u32(ring + at.slot * G::kStage);
+        const uint32_t sfa = smem_u32(scales + (piece & 1) * G::kScales) + 512 * u * F::kAtoms, sfb = sfa + 4096;
 #pragma unroll
         for (int j = 0; j < F::kAtoms; ++j) {
           tc_copy_scales<1>(tmem + G::kSfACol + 4 * j, tc_desc_scales(sfa + 512 * j));
@@ -402,18 +388,18 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           tc_mma<FMT, 1>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(128, BN, F::byte(k)), tmem + G::kSfACol + 4 * F::atom(k),
-                      tmem + G::kSfBCol + 4 * F::atom(k), it > 0 || k > 0);
-        tc_commit<1>(&empty[slot]);
-        if (++slot == l.stages) slot = 0, phase ^= 1;
+                         tmem + G::kSfBCol + 4 * F::atom(k), it > 0 || k > 0);
+        tc_commit<1>(&empty[at.slot]);
+        if (u == F::kPiece - 1) tc_commit<1>(&empty_s[piece++ & 1]);
+        at.next(l.stages);
       }
       tc_commit<1>(&acc_full);
     }
   } else {
     const bool of_w = (warp & 1) == 0;
-    ScaleTurn t{&pass[of_w ? 0 : 2], (warp - 2) >> 1};
-    scale_warp<FMT, false>(of_w ? l.unit_w : l.unit_x, t, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
-                           p.K / F::kGroup, k0, n, ring + G::kA + G::kB + (of_w ? 0 : G::kSfA), G::kStage, l.stages, 512,
-                           full_s, empty, flags);
+    ScaleTurn t{(warp - 2) >> 1};
+    scale_warp<false>(of_w ? l.unit_w : l.unit_x, t, F::kPiece, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
+                      p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, flags);
   }
   __syncwarp();
 
@@ -496,10 +482,10 @@ template <int FMT>
 struct PairGeo {
   using F = TcFormat<FMT>;
   static constexpr int kA = 128 * 128, kB = 128 * 128;
-  static constexpr int kSfA = F::kAtoms * 512, kSfB = F::kAtoms * 1024;
-  static constexpr int kStage = (kA + kB + kSfA + kSfB + 1023) / 1024 * 1024;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kScales = 3 * 4096;  // a slot of the piece ring: 32 bytes of 128 tokens and 256 features
   static constexpr int kTurn = kPairEpilogue * 32 * 33 * 4;  // a padded 32 x 32 block per epilogue warp
-  static constexpr int kSmem = kPairStages * kStage + kTurn + 1024;
+  static constexpr int kSmem = kPairStages * kStage + 2 * kScales + kTurn + 1024;
   static constexpr int kScaleCols = 16 + 32;  // tensor-memory columns of one set of scales; two sets take turns
 };
 
@@ -564,9 +550,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using G = PairGeo<FMT>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kPairStages], full_s[kPairStages], empty[kPairStages], pass[6], acc_full, acc_empty;
+  __shared__ uint64_t full_t[kPairStages], empty[kPairStages], full_s[2], empty_s[2], acc_full, acc_empty;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
+  unsigned char* scales = ring + kPairStages * G::kStage;
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
@@ -576,10 +563,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       mbar_init(&full_t[i], 1);
-      mbar_init(&full_s[i], 2 * 3);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 6; ++i) mbar_init(&pass[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full_s[i], 2 * 3);
+      mbar_init(&empty_s[i], 1);
+    }
     mbar_init(&acc_full, 1);
     mbar_init(&acc_empty, 2 * kPairEpilogue);
     mbar_fence_init();
@@ -615,16 +604,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 9) {
     if (rank == 0 && elect_one()) {
-      unsigned turn = 0, set = 0;
+      unsigned turn = 0, set = 0, piece = 0;
       bool ok = true;
       for (int64_t i = pair; i < l.tiles && ok; i += pairs, turn ^= 1) {
         if (!(ok = mm_wait(&acc_empty, turn ^ 1, flags))) break;
         tc_fence_after();
         for (int kt = 0; kt < nk; ++kt, set ^= 1) {
-          if (!(ok = mm_wait(&full_s[at.slot], at.phase, flags) && mm_wait(&full_t[at.slot], at.phase, flags))) break;
+          const int u = kt % F::kPiece;
+          if (u == 0 && !(ok = mm_wait(&full_s[piece & 1], (piece >> 1) & 1, flags))) break;
+          if (!(ok = mm_wait(&full_t[at.slot], at.phase, flags))) break;
           tc_fence_after();
           const uint32_t st = smem_u32(ring + at.slot * G::kStage);
-          const uint32_t sa = st + G::kA + G::kB, sb = sa + G::kSfA;
+          const uint32_t sa = smem_u32(scales + (piece & 1) * G::kScales) + 512 * u * F::kAtoms;
+          const uint32_t sb = sa + 4096 + 512 * u * F::kAtoms;  // features' words: two blocks a scale word
           const uint32_t ca = tmem + 256 + set * G::kScaleCols, cb = ca + 16;
 #pragma unroll
           for (int j = 0; j < F::kAtoms; ++j) {
@@ -638,6 +630,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc_mma<FMT, 2>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(256, 256, F::byte(k)), ca + 4 * F::atom(k),
                            cb + 8 * F::atom(k), kt > 0 || k > 0);
           tc_commit<2>(&empty[at.slot]);
+          if (u == F::kPiece - 1 || kt == nk - 1) tc_commit<2>(&empty_s[piece++ & 1]);
           at.next(kPairStages);
         }
         tc_commit<2>(&acc_full);
@@ -646,21 +639,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp >= 10) {
     const int block = (warp - 10) >> 1;  // 0: the tokens, 1 and 2: the features' halves
     const bool of_x = block == 0;
-    ScaleTurn t{&pass[2 * block], warp & 1};
+    ScaleTurn t{warp & 1};
     bool ok = true;
     for (int64_t i = pair; i < l.tiles && ok; i += pairs) {
       int64_t m, n;
       pair_tile(l, i, m, n);
-      ok = scale_warp<FMT, true>(of_x ? l.unit_x : l.unit_w, t, of_x ? p.xs : p.ws,
-                                 of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, (int64_t)0,
-                                 nk, ring + G::kA + G::kB + (of_x ? 0 : G::kSfA + (block - 1) * 512), G::kStage, kPairStages,
-                                 of_x ? 512 : 1024, full_s, empty, flags);
+      ok = scale_warp<true>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
+                            of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, 0, nk,
+                            scales + (of_x ? 0 : 4096 + (block - 1) * 512), G::kScales, of_x ? 512 : 1024, full_s, empty_s,
+                            flags);
     }
   } else {
-    float f1, f2;
-    tensor_factors(p, f1, f2);
+    float f1, f2_;
+    tensor_factors(p, f1, f2_);
     const int q = warp & 3, half = warp >> 2;
-    float* turned = reinterpret_cast<float*>(ring + kPairStages * G::kStage) + warp * 32 * 33;
+    float* turned = reinterpret_cast<float*>(scales + 2 * G::kScales) + warp * 32 * 33;
     unsigned turn = 0;
     for (int64_t i = pair; i < l.tiles; i += pairs, turn ^= 1) {
       int64_t m, n;
@@ -672,13 +665,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (!OUT32) {
         uint32_t o[64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          tc_load32(src + 32 * c, v);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[64];
+          tc_load32(src + 64 * c, v);
+          tc_load32(src + 64 * c + 32, v + 32);
           tc_load_wait32(v);
+          tc_load_wait32(v + 32);
+          if (FMT == FMT_NVFP4) {
+            const f2 f = splat(f1);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[16 * c + e] = pack16(__uint_as_float(v[2 * e]) * f1 * f2, __uint_as_float(v[2 * e + 1]) * f1 * f2, p.y_dt);
+            for (int e = 0; e < 32; ++e) {
+              f2 y = mul2(pk(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f);
+              if (f2_ != 1.f) y = mul2(y, splat(f2_));
+              o[32 * c + e] = pack16(lo_of(y), hi_of(y), p.y_dt);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[32 * c + e] = pack16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), p.y_dt);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -704,7 +709,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (lane == 0) mbar_arrive_cluster(&acc_empty, 0);
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f1 * f2);
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f1 * f2_);
           if (l.wide) {
             uint32_t* y = reinterpret_cast<uint32_t*>(p.y) + t * p.N + nn + 32 * c;
 #pragma unroll
@@ -765,13 +770,13 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   l.split = 1;
   while (l.split < 8 && 2 * l.split <= nk && tiles * l.split < sms) l.split *= 2;
   const int64_t per = (nk + l.split - 1) / l.split;
-  const int room = (BN <= 64 ? 110 : 220) * 1024 / G::kStage;
+  const int room = ((BN <= 64 ? 110 : 220) * 1024 - 2 * G::kScales) / G::kStage;
   l.stages = (int)(per < room ? per : room);
   if (l.stages > kMmMaxStages) l.stages = kMmMaxStages;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
   // the partial tile shares the ring's memory
-  int smem = l.stages * G::kStage;
+  int smem = l.stages * G::kStage + 2 * G::kScales;
   if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
   smem += 1024;
   auto kern = k_matmul_tc<FMT, BN>;

@@ -19,6 +19,7 @@ struct TcFormat {
   static constexpr int kGroup = FMT == FMT_NVFP4 ? 16 : 32;
   static constexpr int kScaleBytes = kTileK / kGroup;                     // block scales of a row and K tile: 16, 8 or 4
   static constexpr int kAtoms = kScaleBytes / 4;                          // 4-byte scale words of a row and K tile
+  static constexpr int kPiece = 8 / kAtoms;                               // K tiles of a 32-byte piece of a row's scales
   // Instruction descriptor without the sizes' and scale ids' fields: operand
   // types (E4M3 0, or E2M1 1), E8M0 (1) or E4M3 (0) block scales.
   static constexpr uint32_t kIdesc =
