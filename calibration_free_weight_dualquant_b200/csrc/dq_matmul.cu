@@ -490,18 +490,18 @@ struct PairGeo {
 };
 
 struct PairLaunch {
-  int64_t tiles_m, tiles_n, tiles;
+  unsigned tiles_m, tiles_n, tiles;  // products of 2^31 at most
   int unit_x, unit_w;
   int wide;  // rows of Y start at multiples of 32 bytes
 };
 
 // Tile order: bands of 8 token tiles, features within, so that the pairs at
 // work at one time share operands in L2.
-__device__ __forceinline__ void pair_tile(const PairLaunch& l, int64_t i, int64_t& m, int64_t& n) {
-  const int64_t band = i / (8 * l.tiles_n), rest = i - band * 8 * l.tiles_n;
-  const int64_t height = min((int64_t)8, l.tiles_m - band * 8);
-  m = band * 8 + rest % height;
-  n = rest / height;
+__device__ __forceinline__ void pair_tile(const PairLaunch& l, unsigned i, int64_t& m, int64_t& n) {
+  const unsigned band = i / (8 * l.tiles_n), rest = i - band * 8 * l.tiles_n;
+  const unsigned height = min(8u, l.tiles_m - band * 8), col = rest / height;
+  m = band * 8 + (rest - col * height);
+  n = col;
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int dt) {
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   unsigned char* scales = ring + kPairStages * G::kStage;
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
-  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const unsigned pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   const int nk = (int)((p.K + F::kTileK - 1) / F::kTileK);
   const int64_t nb = p.K / F::kGroup;
   unsigned* flags = &p.hdr->flags;
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (elect_one()) {
       bool ok = true;
       int64_t issued = 0;
-      for (int64_t i = pair; i < l.tiles && ok; i += pairs) {
+      for (unsigned i = pair; i < l.tiles && ok; i += pairs) {
         int64_t m, n;
         pair_tile(l, i, m, n);
         for (int kt = 0; kt < nk; ++kt, ++issued) {
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (rank == 0 && elect_one()) {
       unsigned turn = 0, set = 0, piece = 0;
       bool ok = true;
-      for (int64_t i = pair; i < l.tiles && ok; i += pairs, turn ^= 1) {
+      for (unsigned i = pair; i < l.tiles && ok; i += pairs, turn ^= 1) {
         if (!(ok = mm_wait(&acc_empty, turn ^ 1, flags))) break;
         tc_fence_after();
         for (int kt = 0; kt < nk; ++kt, set ^= 1) {
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const bool of_x = block == 0;
     ScaleTurn t{warp & 1};
     bool ok = true;
-    for (int64_t i = pair; i < l.tiles && ok; i += pairs) {
+    for (unsigned i = pair; i < l.tiles && ok; i += pairs) {
       int64_t m, n;
       pair_tile(l, i, m, n);
       ok = scale_warp<true>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = warp >> 2;
     float* turned = reinterpret_cast<float*>(scales + 2 * G::kScales) + warp * 32 * 33;
     unsigned turn = 0;
-    for (int64_t i = pair; i < l.tiles; i += pairs, turn ^= 1) {
+    for (unsigned i = pair; i < l.tiles; i += pairs, turn ^= 1) {
       int64_t m, n;
       pair_tile(l, i, m, n);
       if (!__all_sync(0xffffffffu, mm_wait(&acc_full, turn, flags))) break;
@@ -671,6 +671,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           tc_load32(src + 64 * c + 32, v + 32);
           tc_load_wait32(v);
           tc_load_wait32(v + 32);
+          if (c == 1) {  // everything is in registers: the next tile's multiply-adds may begin
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(&acc_empty, 0);
+          }
           if (FMT == FMT_NVFP4) {
             const f2 f = splat(f1);
 #pragma unroll
@@ -685,9 +690,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
               o[32 * c + e] = pack16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), p.y_dt);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(&acc_empty, 0);
         if (l.wide) {
           uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + t * p.N + nn;
 #pragma unroll
@@ -814,8 +816,8 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
   if (!encode_codes(&wmap, p.wq, row_bytes, p.N, 128) || !encode_codes(&xmap, p.xq, row_bytes, p.T, 128))
     return cudaErrorInvalidValue;
   PairLaunch l;
-  l.tiles_m = (p.T + 255) / 256;
-  l.tiles_n = (p.N + 255) / 256;
+  l.tiles_m = (unsigned)((p.T + 255) / 256);
+  l.tiles_n = (unsigned)((p.N + 255) / 256);
   l.tiles = l.tiles_m * l.tiles_n;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
@@ -823,7 +825,7 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
   auto kern = k_matmul_pair<FMT, OUT32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t pairs = l.tiles < sms / 2 ? l.tiles : sms / 2;
+  const unsigned pairs = l.tiles < (unsigned)sms / 2 ? l.tiles : (unsigned)sms / 2;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3((unsigned)(2 * pairs));

@@ -26,8 +26,7 @@
 
 namespace dq {
 
-constexpr int kRowThreads = 256;      // dq_glu_quant's block
-constexpr int kNormThreadsMax = 512;  // dq_norm_quant's largest block
+constexpr int kGluThreads = 256;
 constexpr float kFltMax = 3.402823466e38f;
 
 struct RowProblem {
@@ -36,6 +35,7 @@ struct RowProblem {
   const void* g;          // norm weight or NULL
   const void* b_store;    // column inverse scales or NULL
   int col_dt;
+  int b_vec;              // b_store is 16-byte aligned
   int64_t M, K, ld;       // rows, columns, row stride of x and y in elements
   float eps;
   void* h;                // residual sum out (aliases x or y at will) or NULL
@@ -52,12 +52,14 @@ __device__ __forceinline__ float2 h2_values(uint32_t u, int xdt) {
                         : __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-__device__ __forceinline__ uint32_t h2_pack(float lo, float hi, int xdt) {
+// Sum of two packed pairs, rounded once (to nearest even).
+template <int XDT>
+__device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
   uint32_t r;
-  if (xdt == DT_BF16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  if (XDT == DT_BF16)
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -74,7 +76,16 @@ __device__ __forceinline__ void h8_values(const uint4& v, float* x) {
 
 // The 8 column scales at col (1 where there are none).
 __device__ __forceinline__ void b8_values(const RowProblem& p, int64_t col, float* b) {
-  if (p.b_store) {
+  if (p.b_vec) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.b_store) + col));
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = h2_values(u[i], p.col_dt);
+      b[2 * i] = f.x;
+      b[2 * i + 1] = f.y;
+    }
+  } else if (p.b_store) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = b_decode(p.b_store, p.col_dt, col + i);
   } else {
@@ -86,6 +97,13 @@ __device__ __forceinline__ void b8_values(const RowProblem& p, int64_t col, floa
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Three-input maximum that propagates NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -158,71 +176,99 @@ __device__ __forceinline__ uint32_t no_negzero(uint32_t w) {
   return w & (0x77777777u | (w << 1) | (w << 2) | (w << 3));
 }
 
-// Quantizes and stores the 8 elements of a lane at (row, col).  v: fp32 values
-// of x' known to a relative delta/2; exact(x64) gives the fp64 ones.  `force`
-// (the same for a group's lanes) decides in fp64 throughout.  Every lane of the
-// warp calls it (shuffles); `on` lanes hold data, the others zeros.  A group
-// with a value that is not finite in fp32 gets the format's NaN scale and zero
-// codes.  A group of zeros takes the fp64 path too (its scale is 1 only if no
-// product underflowed).
-template <int FMT, class Exact>
-__device__ __forceinline__ bool quant_store8(const RowProblem& p, int64_t row, int64_t col, bool on, const f2* v,
-                                             float delta, float sT, float isT, bool force, Exact&& exact) {
-  constexpr int LG = group_lanes(FMT);
-  constexpr double qmax = grid_qmax(FMT);
-  const int lane = threadIdx.x & 31;
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max_nan(m, max_nan(fabsf(lo_of(v[i])), fabsf(hi_of(v[i]))));
-#pragma unroll
-  for (int o = 1; o < LG; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  bool amb = force, bad = false;
-  float a = a_fast<FMT>(m, (float)qmax, isT, amb);  // flags a NaN or an infinity too
-  amb &= on;
-  double x64[8];
-  bool have64 = false;
-  if (__any_sync(0xffffffffu, amb)) {  // next to a projection midpoint or out of the trusted range: about 1 group in 2^17
-    double m64 = 0.0;
-    if (on) {
-      exact(x64);
-      have64 = true;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m64 = fmax(m64, fabs(x64[i]) <= (double)kFltMax ? fabs(x64[i]) : CUDART_INF);
+// fp64 values of 8 elements of x' at (row, col), from the stored inputs.
+template <int XDT, bool GLU>
+__device__ __forceinline__ void exact8(const RowProblem& p, int64_t row, int64_t col, double rstd, double* x) {
+  const uint16_t* src = reinterpret_cast<const uint16_t*>(GLU ? p.x : (p.y ? p.h : p.x));
+  float h[8], b[8], g[8];
+  h8_values<XDT>(*reinterpret_cast<const uint4*>(src + row * p.ld + col), h);
+  b8_values(p, col, b);
+  if (GLU) {
+    h8_values<XDT>(*reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.y) + row * p.ld + col), g);
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const double d = (double)h[i];
+      x[i] = d / (1.0 + exp(-d)) * ((double)g[i] * (double)b[i]);
     }
-#pragma unroll
-    for (int o = 1; o < LG; o <<= 1) m64 = fmax(m64, __shfl_xor_sync(0xffffffffu, m64, o));
-    if (amb) {
-      bad = m64 > (double)kFltMax;
-      a = m64 == 0.0 || bad ? 1.f : (float)a_project<FMT>(m64 / qmax, (double)sT);
-    }
-  }
-  if (!on) return false;
-  const float ia = fmt_pow2(FMT) ? __uint_as_float(0x7F000000u - __float_as_uint(a)) : __frcp_rn(a);
-  uint32_t cw[2], cl[2];
-  codes_fast<FMT>(v, FMT == FMT_NVFP4 ? isT * ia * (1.f - delta) : ia * (1.f - delta), cl);
-  codes_fast<FMT>(v, FMT == FMT_NVFP4 ? isT * ia * (1.f + delta) : ia * (1.f + delta), cw);
-  if (bad) {
-    cw[0] = cw[1] = 0;
-  } else if (amb || cl[0] != cw[0] || cl[1] != cw[1]) {
-    if (!have64) exact(x64);
-    codes_exact<FMT>(x64, FMT == FMT_NVFP4 ? (double)sT * (double)a : (double)a, cw);
   } else {
-    cw[0] = no_negzero<FMT>(cw[0]);
-    if (FMT == FMT_MXFP8) cw[1] = no_negzero<FMT>(cw[1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = 1.f;
+    if (p.g) h8_values<XDT>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.g) + col)), g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (double)h[i] * ((double)g[i] * (double)b[i]) * rstd;
   }
+}
+
+// The lane's codes (8 bytes, or 4 in cw[0]) and its group's scale to memory.
+template <int FMT>
+__device__ __forceinline__ void store8(const RowProblem& p, int64_t row, int64_t col, const uint32_t* cw, float a, bool bad) {
+  constexpr int LG = group_lanes(FMT);
   const int64_t at = row * p.K + col;
   if (FMT == FMT_MXFP8)
     *reinterpret_cast<uint2*>(p.codes + at) = make_uint2(cw[0], cw[1]);
   else
     *reinterpret_cast<uint32_t*>(p.codes + (at >> 1)) = cw[0];
-  if ((lane & (LG - 1)) == 0) {
+  if ((threadIdx.x & (LG - 1)) == 0) {
     unsigned char* s = p.scales + row * p.nb + col / (8 * LG);
     if (bad)
       *s = fmt_pow2(FMT) ? 0xFFu : 0x7Fu;
     else
       a_store_f<FMT>(s, 0, a);
   }
+}
+
+// A warp's 32 x 8 elements decided in fp64 throughout and stored: the cold path,
+// out of line.  A group with a value that is not finite in fp32 gets the
+// format's NaN scale and zero codes; returns whether the lane's group did.
+template <int FMT, int XDT, bool GLU>
+static __device__ __noinline__ bool quant_exact(const RowProblem& p, int64_t row, int64_t col, bool on, double rstd, float sT) {
+  constexpr int LG = group_lanes(FMT);
+  double x[8], m = 0.0;
+  if (on) {
+    exact8<XDT, GLU>(p, row, col, rstd, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmax(m, fabs(x[i]) <= (double)kFltMax ? fabs(x[i]) : CUDART_INF);
+  }
+#pragma unroll
+  for (int o = 1; o < LG; o <<= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!on) return false;
+  const bool bad = m > (double)kFltMax;
+  const float a = m == 0.0 || bad ? 1.f : (float)a_project<FMT>(m / grid_qmax(FMT), (double)sT);
+  uint32_t cw[2] = {0u, 0u};
+  if (!bad) codes_exact<FMT>(x, FMT == FMT_NVFP4 ? (double)sT * (double)a : (double)a, cw);
+  store8<FMT>(p, row, col, cw, a, bad);
   return bad;
+}
+
+// Quantizes and stores the 8 elements of a lane at (row, col).  v: fp32 values
+// of x' known to a relative delta/2.  `force` sends the warp to fp64.  Every
+// lane of the warp calls it; `on` lanes hold data, the others zeros.  One
+// undecided lane sends the whole warp to fp64 (about one call in 100 at most):
+// zeros go there too, as their scale is 1 only if no product underflowed.
+template <int FMT, int XDT, bool GLU>
+__device__ __forceinline__ bool quant_store8(const RowProblem& p, int64_t row, int64_t col, bool on, const f2* v, float delta,
+                                             float sT, float isT, bool force, double rstd) {
+  constexpr int LG = group_lanes(FMT);
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max3_nan(m, fabsf(lo_of(v[i])), fabsf(hi_of(v[i])));
+#pragma unroll
+  for (int o = 1; o < LG; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  bool redo = force;
+  const float a = a_fast<FMT>(m, (float)grid_qmax(FMT), isT, redo);  // flags a NaN or an infinity too
+  const float ia = fmt_pow2(FMT) ? __uint_as_float(0x7F000000u - __float_as_uint(a)) : __frcp_rn(a);
+  const float c = FMT == FMT_NVFP4 ? isT * ia : ia;
+  uint32_t cw[2], cl[2];
+  codes_fast<FMT>(v, c * (1.f - delta), cl);
+  codes_fast<FMT>(v, c * (1.f + delta), cw);
+  redo |= cl[0] != cw[0] || cl[1] != cw[1];
+  if (__any_sync(0xffffffffu, redo && on)) return quant_exact<FMT, XDT, GLU>(p, row, col, on, rstd, sT);
+  if (on) {
+    cw[0] = no_negzero<FMT>(cw[0]);
+    if (FMT == FMT_MXFP8) cw[1] = no_negzero<FMT>(cw[1]);
+    store8<FMT>(p, row, col, cw, a, false);
+  }
+  return false;
 }
 
 // Grid-wide barrier of a cooperative launch (bounded wait).
@@ -256,10 +302,11 @@ __device__ __forceinline__ void amax_to_header(WsHeader* hdr, double amax) {
 
 // ---------------------------------------------------------------------------
 // dq_norm_quant: a CTA takes rows grid-stride, thread t the 8-element chunks
-// t, t + blockDim, ...; with NC > 0 every thread has at most NC chunks and
-// keeps the row and its g b in registers, with NC = 0 (rows longer than 4 x
-// 512 chunks) it reads the stored row again after the sum.  The sum of
-// squares is held in fp64.
+// t, t + blockDim, ...  With NC = 1, 2 or 4 a thread has at most NC chunks and
+// keeps its part of the row in registers; with NC = 1 and 2 it also reads the
+// next row while it works on this one, and with NC = 1 it keeps g b.  NC = 0
+// is for rows longer than 4 x 1024 chunks: the stored row is read again after
+// the sum.  The sum of squares is held in fp64.
 
 template <int XDT>
 __device__ __forceinline__ void gb8(const RowProblem& p, int64_t col, float* gb) {
@@ -272,36 +319,14 @@ __device__ __forceinline__ void gb8(const RowProblem& p, int64_t col, float* gb)
   }
 }
 
-// fp64 values of 8 elements of x' from the stored row (cold path).
-template <int XDT>
-static __device__ __noinline__ void norm_exact8(const RowProblem& p, const uint4& hv, int64_t col, double rstd, double* x) {
-  float h[8], b[8], g[8];
-  h8_values<XDT>(hv, h);
-  b8_values(p, col, b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) g[i] = 1.f;
-  if (p.g) h8_values<XDT>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.g) + col)), g);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (double)h[i] * ((double)g[i] * (double)b[i]) * rstd;
+__device__ __forceinline__ uint4 load16(const void* base, int64_t off) {
+  return *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + off);
 }
 
-// h of the 8 elements at `off`: x + r rounded to the input type, stored.
+// h = x + r, rounded to the input type.
 template <int XDT>
-__device__ __forceinline__ uint4 norm_load8(const RowProblem& p, int64_t off) {
-  uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.x) + off);
-  if (p.y) {
-    const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.y) + off);
-    uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = h2_values(u[i], XDT), c = h2_values(w[i], XDT);
-      u[i] = h2_pack(a.x + c.x, a.y + c.y, XDT);
-    }
-    v = make_uint4(u[0], u[1], u[2], u[3]);
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + off) = v;
-  }
-  return v;
+__device__ __forceinline__ uint4 add8(const uint4& x, const uint4& r) {
+  return make_uint4(h2_add<XDT>(x.x, r.x), h2_add<XDT>(x.y, r.y), h2_add<XDT>(x.z, r.z), h2_add<XDT>(x.w, r.w));
 }
 
 // 1/rms of the row from the threads' partial sums of squares; NaN for a row
@@ -325,23 +350,48 @@ __device__ __forceinline__ double row_rstd(double s, double* red, const RowProbl
   return red[32];
 }
 
+// Largest finite |x'| of a lane's 8 elements, in fp64.
+template <int XDT, bool GLU>
+static __device__ __noinline__ double amax_exact(const RowProblem& p, int64_t row, int64_t col, double rstd) {
+  double x[8], m = 0.0;
+  exact8<XDT, GLU>(p, row, col, rstd, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (fabs(x[i]) <= (double)kFltMax) m = fmax(m, fabs(x[i]));
+  return m;
+}
+
 template <int FMT, int XDT, int NC>
-__global__ void __launch_bounds__(kNormThreadsMax) k_norm(RowProblem p) {
+__global__ void __launch_bounds__(NC == 1 || NC == 2 ? 512 : 1024, NC == 1 || NC == 2 ? 2 : 1)
+    k_norm(const __grid_constant__ RowProblem p) {
   __shared__ double red[33];
   constexpr int N = NC > 0 ? NC : 1;
+  constexpr bool AHEAD = NC == 1 || NC == 2, KEEP = NC == 1;
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int64_t chunks = p.K / 8;
-  const int64_t trips = (chunks + nt - 1) / nt;
-  const uint16_t* hsrc = reinterpret_cast<const uint16_t*>(p.y ? p.h : p.x);
+  const int chunks = (int)(p.K / 8);
+  const int trips = NC > 0 ? 1 : (chunks + nt - 1) / nt;
+  const void* hsrc = p.y ? p.h : p.x;
   float gb[N][8];
-  if (NC > 0) {
+  auto get_gb = [&](int c, int ch) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gb[c][i] = 0.f;
+    if (ch < chunks) gb8<XDT>(p, ch * 8, gb[c]);
+  };
+  uint4 xv[N], rv[N];  // the next row's inputs
+  auto read = [&](int64_t row) {
 #pragma unroll
     for (int c = 0; c < N; ++c) {
-      const int64_t ch = tid + (int64_t)c * nt;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) gb[c][i] = 0.f;
-      if (ch < chunks) gb8<XDT>(p, ch * 8, gb[c]);
+      const int ch = tid + c * nt;
+      xv[c] = rv[c] = make_uint4(0, 0, 0, 0);
+      if (row < p.M && ch < chunks) {
+        xv[c] = load16(p.x, row * p.K + ch * 8);
+        if (p.y) rv[c] = load16(p.y, row * p.K + ch * 8);
+      }
     }
+  };
+  if (AHEAD) {
+    read(blockIdx.x);
+    if (KEEP) get_gb(0, tid);
   }
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
@@ -360,26 +410,38 @@ __global__ void __launch_bounds__(kNormThreadsMax) k_norm(RowProblem p) {
     }
 #pragma unroll 1
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-      const int64_t base = row * p.ld;
       double rstd;
       if (FMT != FMT_NVFP4 || pass == 0) {
         double s = 0.0;
 #pragma unroll 1
-        for (int64_t t = 0; t < (NC > 0 ? 1 : trips); ++t) {
+        for (int t = 0; t < trips; ++t) {
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            const int64_t ch = tid + (NC > 0 ? (int64_t)c : t) * nt;
-            hv[c] = make_uint4(0, 0, 0, 0);
-            if (ch < chunks) hv[c] = norm_load8<XDT>(p, base + ch * 8);
+            const int ch = tid + (NC > 0 ? c : t) * nt;
+            if (!AHEAD) {
+              xv[c] = rv[c] = make_uint4(0, 0, 0, 0);
+              if (ch < chunks) {
+                xv[c] = load16(p.x, row * p.K + ch * 8);
+                if (p.y) rv[c] = load16(p.y, row * p.K + ch * 8);
+              }
+            }
           }
 #pragma unroll
           for (int c = 0; c < N; ++c) {
+            const int ch = tid + (NC > 0 ? c : t) * nt;
+            hv[c] = xv[c];
+            if (p.y) {
+              hv[c] = add8<XDT>(xv[c], rv[c]);
+              if (ch < chunks)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + row * p.K + ch * 8) = hv[c];
+            }
             float h[8];
             h8_values<XDT>(hv[c], h);
 #pragma unroll
             for (int i = 0; i < 8; ++i) s = fma((double)h[i], (double)h[i], s);
           }
         }
+        if (AHEAD) read(row + gridDim.x);
         rstd = row_rstd(s, red, p);
         if (FMT == FMT_NVFP4 && tid == 0) p.rstd[row] = rstd;
       } else {
@@ -388,45 +450,32 @@ __global__ void __launch_bounds__(kNormThreadsMax) k_norm(RowProblem p) {
       const float rs = (float)rstd;
       const bool rs_ok = rs >= 0x1p-100f && rs <= 0x1p100f;
 #pragma unroll 1
-      for (int64_t t = 0; t < (NC > 0 ? 1 : trips); ++t) {
+      for (int t = 0; t < trips; ++t) {
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          const int64_t ch = tid + (NC > 0 ? (int64_t)c : t) * nt;
+          const int ch = tid + (NC > 0 ? c : t) * nt;
           const bool on = ch < chunks;
           if (NC == 0 || (FMT == FMT_NVFP4 && pass == 1))
-            hv[c] = on ? *reinterpret_cast<const uint4*>(hsrc + base + ch * 8) : make_uint4(0, 0, 0, 0);
-          if (NC == 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) gb[c][i] = 0.f;
-            if (on) gb8<XDT>(p, ch * 8, gb[c]);
-          }
+            hv[c] = on ? load16(hsrc, row * p.K + ch * 8) : make_uint4(0, 0, 0, 0);
+          if (!KEEP) get_gb(c, ch);
           float h[8];
           h8_values<XDT>(hv[c], h);
+          f2 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = on ? mul2(mul2(pk(h[2 * i], h[2 * i + 1]), splat(rs)), pk(gb[c][2 * i], gb[c][2 * i + 1])) : 0ull;
           if (FMT == FMT_NVFP4 && pass == 0) {
             // values that are not finite have no share in the tensor scale
             if (on && rstd == rstd) {
               float mf = 0.f;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) mf = max_nan(mf, fabsf((h[i] * rs) * gb[c][i]));
-              double x[8], m = 0.0;
-              if (rs_ok && mf >= 0x1p-60f && mf <= kFltMax) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = fmax(m, fabs((double)h[i] * (double)gb[c][i]));  // exact products
-                amax = fmax(amax, m * rstd);
-              } else {
-                norm_exact8<XDT>(p, hv[c], ch * 8, rstd, x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (fabs(x[i]) <= (double)kFltMax) amax = fmax(amax, fabs(x[i]));
-              }
+              for (int i = 0; i < 4; ++i) mf = max3_nan(mf, fabsf(lo_of(v[i])), fabsf(hi_of(v[i])));
+              // fp64 only where the fp32 value could raise the maximum
+              if (!((double)mf * (1.0 + 0x1p-18) < amax) || !rs_ok || (mf < 0x1p-60f && amax < 0x1p-59))
+                amax = fmax(amax, amax_exact<XDT, false>(p, row, ch * 8, rstd));
             }
           } else {
-            f2 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              v[i] = on ? mul2(mul2(pk(h[2 * i], h[2 * i + 1]), splat(rs)), pk(gb[c][2 * i], gb[c][2 * i + 1])) : 0ull;
-            bad |= quant_store8<FMT>(p, row, ch * 8, on, v, 0x1p-20f, sT, isT, !sT_ok || !rs_ok,
-                                     [&](double* x) { norm_exact8<XDT>(p, hv[c], ch * 8, rstd, x); });
+            bad |= quant_store8<FMT, XDT, false>(p, row, ch * 8, on, v, 0x1p-20f, sT, isT, !sT_ok || !rs_ok, rstd);
           }
         }
       }
@@ -438,21 +487,8 @@ __global__ void __launch_bounds__(kNormThreadsMax) k_norm(RowProblem p) {
 
 // ---------------------------------------------------------------------------
 // dq_glu_quant: elementwise but for the groups, so the warps of the grid take
-// items of 32 x 8 consecutive columns of a row, row-major and grid-stride.
-
-// fp64 values of 8 elements (cold path).
-template <int XDT>
-static __device__ __noinline__ void glu_exact8(const RowProblem& p, const uint4& gv, const uint4& uv, int64_t col, double* x) {
-  float g[8], u[8], b[8];
-  h8_values<XDT>(gv, g);
-  h8_values<XDT>(uv, u);
-  b8_values(p, col, b);
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i) {
-    const double d = (double)g[i];
-    x[i] = d / (1.0 + exp(-d)) * ((double)u[i] * (double)b[i]);
-  }
-}
+// items of 32 x 8 consecutive columns of a row, row-major and grid-stride, and
+// read the next item while they work on one.
 
 // x' in fp32: relative error below 10 * 2^-24 (expf within 2 ulp, six further
 // roundings) while exp(-gate) and up * b stay in range; `far` marks the rest.
@@ -477,14 +513,12 @@ __device__ __forceinline__ void glu_fast8(const uint4& gv, const uint4& uv, cons
 }
 
 template <int FMT, int XDT>
-__global__ void __launch_bounds__(kRowThreads) k_glu(RowProblem p) {
+__global__ void __launch_bounds__(kGluThreads, 4) k_glu(const __grid_constant__ RowProblem p) {
   const int lane = threadIdx.x & 31;
   const int64_t spans = (p.K + 255) / 256;  // 256-column pieces of a row
-  const int64_t items = p.M * spans;
-  const int64_t w0 = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t nw = (int64_t)gridDim.x * (kRowThreads / 32);
-  const uint16_t* gate = reinterpret_cast<const uint16_t*>(p.x);
-  const uint16_t* up = reinterpret_cast<const uint16_t*>(p.y);
+  const int64_t w0 = (int64_t)blockIdx.x * (kGluThreads / 32) + (threadIdx.x >> 5);
+  const int64_t nw = (int64_t)gridDim.x * (kGluThreads / 32);
+  const int64_t drow = nw / spans, dspan = nw - drow * spans;  // the grid's stride as rows and spans
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
@@ -498,44 +532,46 @@ __global__ void __launch_bounds__(kRowThreads) k_glu(RowProblem p) {
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
+    int64_t row = w0 / spans, span = w0 - row * spans;
+    uint4 gn, un;
+    auto read = [&]() {
+      const int64_t col = span * 256 + lane * 8;
+      gn = un = make_uint4(0, 0, 0, 0);
+      if (row < p.M && col < p.K) {
+        gn = load16(p.x, row * p.ld + col);
+        un = load16(p.y, row * p.ld + col);
+      }
+    };
+    read();
 #pragma unroll 1
-    for (int64_t w = w0; w < items; w += nw) {
-      const int64_t row = w / spans, col = (w - row * spans) * 256 + lane * 8;
+    while (row < p.M) {
+      const int64_t r = row, col = span * 256 + lane * 8;
       const bool on = col < p.K;
-      uint4 gv = make_uint4(0, 0, 0, 0), uv = gv;
+      const uint4 gv = gn, uv = un;
+      row += drow;
+      span += dspan;
+      if (span >= spans) {
+        span -= spans;
+        ++row;
+      }
+      read();
       float b[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[i] = 0.f;
-      if (on) {
-        gv = __ldg(reinterpret_cast<const uint4*>(gate + row * p.ld + col));
-        uv = __ldg(reinterpret_cast<const uint4*>(up + row * p.ld + col));
-        b8_values(p, col, b);
-      }
+      if (on) b8_values(p, col, b);
       f2 v[4];
       bool far = false;
       glu_fast8<XDT>(gv, uv, b, v, far);
-      if (far) {  // fp64, then rounded once
-        double x[8];
-        glu_exact8<XDT>(p, gv, uv, col, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = pk((float)x[2 * i], (float)x[2 * i + 1]);
-      }
       if (FMT == FMT_NVFP4 && pass == 0) {
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max_nan(m, max_nan(fabsf(lo_of(v[i])), fabsf(hi_of(v[i]))));
+        for (int i = 0; i < 4; ++i) m = max3_nan(m, fabsf(lo_of(v[i])), fabsf(hi_of(v[i])));
         // fp64 only where the fp32 value could raise the maximum; values that
         // are not finite have no share in it
-        if (on && (!((double)m * (1.0 + 0x1p-18) < amax) || (m < 0x1p-60f && amax < 0x1p-59))) {
-          double x[8];
-          glu_exact8<XDT>(p, gv, uv, col, x);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (fabs(x[i]) <= (double)kFltMax) amax = fmax(amax, fabs(x[i]));
-        }
+        if (on && (far || !((double)m * (1.0 + 0x1p-18) < amax) || (m < 0x1p-60f && amax < 0x1p-59)))
+          amax = fmax(amax, amax_exact<XDT, true>(p, r, col, 0.0));
       } else {
-        bad |= quant_store8<FMT>(p, row, col, on, v, 0x1p-19f, sT, isT, !sT_ok,
-                                 [&](double* x) { glu_exact8<XDT>(p, gv, uv, col, x); });
+        bad |= quant_store8<FMT, XDT, true>(p, r, col, on, v, 0x1p-19f, sT, isT, !sT_ok || far, 0.0);
       }
     }
   }
@@ -567,8 +603,8 @@ static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, boo
 template <int FMT, int XDT>
 static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
   const int64_t chunks = p.K / 8;
-  const int nc = chunks <= kNormThreadsMax ? 1 : (chunks <= 2 * kNormThreadsMax ? 2 : (chunks <= 4 * kNormThreadsMax ? 4 : 0));
-  const int64_t per = nc > 0 ? (chunks + nc - 1) / nc : kNormThreadsMax;
+  const int nc = chunks <= 512 ? 1 : (chunks <= 1024 ? 2 : (chunks <= 4096 ? 4 : 0));
+  const int64_t per = nc > 0 ? (chunks + nc - 1) / nc : 1024;
   const int threads = (int)((per + 31) / 32 * 32);
   void (*kern)(RowProblem) = nc == 1   ? k_norm<FMT, XDT, 1>
                              : nc == 2 ? k_norm<FMT, XDT, 2>
@@ -580,7 +616,7 @@ static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
 template <int FMT, int XDT>
 static cudaError_t glu_launch(const RowProblem& p, int sms, cudaStream_t st) {
   const int64_t items = p.M * ((p.K + 255) / 256);
-  return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kRowThreads, sms, st);
+  return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, sms, st);
 }
 
 // Checks shared by the two entry points.
@@ -611,6 +647,7 @@ static void row_fill(RowProblem* p, int64_t rows, int64_t cols, const void* col_
                      const dq_outputs* out, void* workspace) {
   p->b_store = col_scales;
   p->col_dt = col_dtype;
+  p->b_vec = col_scales != nullptr && (uintptr_t)col_scales % 16 == 0;
   p->M = rows;
   p->K = cols;
   p->codes = static_cast<unsigned char*>(out->codes);
