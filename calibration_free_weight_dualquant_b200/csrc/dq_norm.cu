@@ -12,10 +12,15 @@
 //   a = Proj_Fa(max|x'| over the group / qmax), 1 for an all-zero group
 //   q = Q(x' / a), ties to even, clipped
 // x' is not rounded on the way: the decisions are those of the real numbers.
-// fp32 values known to a relative 2^-20 (norm) or 2^-19 (glu) settle nearly
-// all of them: a code is certain where both ends of that bracket convert to
-// it, a block scale where the fp32 ratio is not next to a projection midpoint.
-// The rest is decided in fp64 from the stored inputs.
+// fp32 values known to a relative 2^-20 settle nearly all of them: a code is
+// certain where both ends of a bracket that wide convert to it, a block scale
+// where the fp32 ratio is not next to a projection midpoint.  The rest is
+// decided in fp64 from the stored inputs.
+//
+// A lane holds 16 consecutive elements: a whole NVFP4 group, or half a group of
+// the MX formats.  (With 8 a lane, twice as many lanes repeated the scale's
+// arithmetic, the votes and the address arithmetic: 34 and 58 instructions an
+// element, measured, and the issue slots were the bound.)
 #include <climits>
 #include <math_constants.h>
 
@@ -36,6 +41,8 @@ struct RowProblem {
   const void* b_store;    // column inverse scales or NULL
   int col_dt;
   int b_vec;              // b_store is 16-byte aligned
+  int wide;               // rows of x, y and h start at multiples of 32 bytes
+  int codes_vec;          // codes is 16-byte aligned
   int64_t M, K, ld;       // rows, columns, row stride of x and y in elements
   float eps;
   void* h;                // residual sum out (aliases x or y at will) or NULL
@@ -63,34 +70,87 @@ __device__ __forceinline__ uint32_t h2_add(uint32_t a, uint32_t b) {
   return r;
 }
 
-template <int XDT>
-__device__ __forceinline__ void h8_values(const uint4& v, float* x) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+// 16 consecutive 16-bit elements of a lane.
+struct V16 {
+  uint32_t u[8];
+};
+__device__ __forceinline__ V16 zero16() {
+  V16 v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = h2_values(u[i], XDT);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
+  for (int i = 0; i < 8; ++i) v.u[i] = 0;
+  return v;
+}
+// An input of the call, read once: free to move above stores (a store of h to
+// the input's own place depends on the value loaded from it).
+__device__ __forceinline__ V16 load16(const void* base, int64_t off, bool wide) {
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + off;
+  V16 v;
+  if (wide) {
+    asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]), "=r"(v.u[4]), "=r"(v.u[5]), "=r"(v.u[6]), "=r"(v.u[7])
+        : "l"(p));
+  } else {
+    asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "l"(p));
+    asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.u[4]), "=r"(v.u[5]), "=r"(v.u[6]), "=r"(v.u[7]) : "l"(p + 8));
+  }
+  return v;
+}
+// What this thread stored earlier, or an input read again after stores.
+__device__ __forceinline__ V16 load16_again(const void* base, int64_t off) {
+  const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + off;
+  V16 v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.u[4 * i]), "=r"(v.u[4 * i + 1]), "=r"(v.u[4 * i + 2]), "=r"(v.u[4 * i + 3])
+                 : "l"(p + 8 * i)
+                 : "memory");
+  return v;
+}
+__device__ __forceinline__ void store16(void* base, int64_t off, bool wide, const V16& v) {
+  uint16_t* p = reinterpret_cast<uint16_t*>(base) + off;
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.u[0]), "r"(v.u[1]), "r"(v.u[2]),
+                 "r"(v.u[3]), "r"(v.u[4]), "r"(v.u[5]), "r"(v.u[6]), "r"(v.u[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(v.u[0], v.u[1], v.u[2], v.u[3]);
+    *reinterpret_cast<uint4*>(p + 8) = make_uint4(v.u[4], v.u[5], v.u[6], v.u[7]);
+  }
+}
+// All 16 are zeros (of either sign).
+__device__ __forceinline__ bool zero_bits16(const V16& v) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) any |= v.u[i];
+  return (any & 0x7FFF7FFFu) == 0;
+}
+// The elements as fp32 pairs.
+template <int XDT>
+__device__ __forceinline__ void pairs16(const V16& v, f2* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = h2_values(v.u[i], XDT);
+    x[i] = pk(f.x, f.y);
   }
 }
 
-// The 8 column scales at col (1 where there are none).
-__device__ __forceinline__ void b8_values(const RowProblem& p, int64_t col, float* b) {
+// The 16 column scales at col (1 where there are none).
+__device__ __forceinline__ void b16_values(const RowProblem& p, int64_t col, f2* b) {
   if (p.b_vec) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.b_store) + col));
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.b_store) + col);
+    const uint4 v0 = __ldg(q), v1 = __ldg(q + 1);
+    const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const float2 f = h2_values(u[i], p.col_dt);
-      b[2 * i] = f.x;
-      b[2 * i + 1] = f.y;
+      b[i] = pk(f.x, f.y);
     }
-  } else if (p.b_store) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = b_decode(p.b_store, p.col_dt, col + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = 1.f;
+    for (int i = 0; i < 8; ++i)
+      b[i] = p.b_store ? pk(b_decode(p.b_store, p.col_dt, col + 2 * i), b_decode(p.b_store, p.col_dt, col + 2 * i + 1))
+                       : splat(1.f);
   }
 }
 
@@ -107,8 +167,10 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return d;
 }
 
-// Lanes of a group at 8 elements a lane.
-__host__ __device__ constexpr int group_lanes(int fmt) { return fmt == FMT_NVFP4 ? 2 : 4; }
+// Lanes of a group at 16 elements a lane.
+__host__ __device__ constexpr int group_lanes(int fmt) { return fmt == FMT_NVFP4 ? 1 : 2; }
+// 32-bit words of a lane's codes.
+__host__ __device__ constexpr int code_words(int fmt) { return fmt == FMT_MXFP8 ? 4 : 2; }
 
 // Magnitude code of |x'| = ax for the scale a (a = s_T e for NVFP4), decided in
 // fp64: E2M1 midpoints times a are exact (3 + 28 significant bits), a division
@@ -125,47 +187,33 @@ __device__ __forceinline__ uint32_t mag_code(double ax, double a) {
          (ax > 5.0 * a);
 }
 
-// Codes of 8 elements from their fp64 values: 8 bytes, or 8 nibbles in cw[0].
-template <int FMT>
-__device__ __forceinline__ void codes_exact(const double* x, double a, uint32_t* cw) {
-  cw[0] = cw[1] = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t m = mag_code<FMT>(fabs(x[i]), a);
-    const uint32_t neg = m != 0 && x[i] < 0.0;
-    if (FMT == FMT_MXFP8)
-      cw[i >> 2] |= (m | (neg << 7)) << (8 * (i & 3));
-    else
-      cw[0] |= (m | (neg << 3)) << (4 * i);
-  }
-}
-
-// Eight packed conversions of v[0..7] times s: E4M3 bytes or E2M1 nibbles
-// (hardware round to nearest even, saturating).
+// Conversions of v[0 .. 15] times s: E4M3 bytes or E2M1 nibbles (hardware round
+// to nearest even, saturating).
 template <int FMT>
 __device__ __forceinline__ void codes_fast(const f2* v, float s, uint32_t* cw) {
   const f2 ss = splat(s);
-  f2 t[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t[i] = mul2(v[i], ss);
-  if (FMT == FMT_MXFP8) {
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
+  for (int w = 0; w < code_words(FMT); ++w) {
+    if (FMT == FMT_MXFP8) {
+      const f2 a = mul2(v[2 * w], ss), b = mul2(v[2 * w + 1], ss);
       asm("{\n.reg .b16 l, h;\ncvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\ncvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n"
           "mov.b32 %0, {l, h};\n}"
-          : "=r"(cw[c])
-          : "f"(lo_of(t[2 * c])), "f"(hi_of(t[2 * c])), "f"(lo_of(t[2 * c + 1])), "f"(hi_of(t[2 * c + 1])));
-  } else {
-    asm("{\n.reg .b8 c0, c1, c2, c3;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n"
-        "mov.b32 %0, {c0, c1, c2, c3};\n}"
-        : "=r"(cw[0])
-        : "f"(lo_of(t[0])), "f"(hi_of(t[0])), "f"(lo_of(t[1])), "f"(hi_of(t[1])), "f"(lo_of(t[2])), "f"(hi_of(t[2])),
-          "f"(lo_of(t[3])), "f"(hi_of(t[3])));
-    cw[1] = 0;
+          : "=r"(cw[w])
+          : "f"(lo_of(a)), "f"(hi_of(a)), "f"(lo_of(b)), "f"(hi_of(b)));
+    } else {
+      f2 t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = mul2(v[4 * w + i], ss);
+      asm("{\n.reg .b8 c0, c1, c2, c3;\n"
+          "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n"
+          "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n"
+          "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n"
+          "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n"
+          "mov.b32 %0, {c0, c1, c2, c3};\n}"
+          : "=r"(cw[w])
+          : "f"(lo_of(t[0])), "f"(hi_of(t[0])), "f"(lo_of(t[1])), "f"(hi_of(t[1])), "f"(lo_of(t[2])), "f"(hi_of(t[2])),
+            "f"(lo_of(t[3])), "f"(hi_of(t[3])));
+    }
   }
 }
 
@@ -176,99 +224,108 @@ __device__ __forceinline__ uint32_t no_negzero(uint32_t w) {
   return w & (0x77777777u | (w << 1) | (w << 2) | (w << 3));
 }
 
-// fp64 values of 8 elements of x' at (row, col), from the stored inputs.
+// fp64 value of x' at (row, col), from the stored inputs.
 template <int XDT, bool GLU>
-__device__ __forceinline__ void exact8(const RowProblem& p, int64_t row, int64_t col, double rstd, double* x) {
-  const uint16_t* src = reinterpret_cast<const uint16_t*>(GLU ? p.x : (p.y ? p.h : p.x));
-  float h[8], b[8], g[8];
-  h8_values<XDT>(*reinterpret_cast<const uint4*>(src + row * p.ld + col), h);
-  b8_values(p, col, b);
-  if (GLU) {
-    h8_values<XDT>(*reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.y) + row * p.ld + col), g);
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const double d = (double)h[i];
-      x[i] = d / (1.0 + exp(-d)) * ((double)g[i] * (double)b[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = 1.f;
-    if (p.g) h8_values<XDT>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.g) + col)), g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (double)h[i] * ((double)g[i] * (double)b[i]) * rstd;
-  }
+__device__ __forceinline__ double exact1(const RowProblem& p, int64_t row, int64_t col, double rstd) {
+  const double h = (double)b_decode(GLU ? p.x : (p.y ? p.h : p.x), XDT, row * p.ld + col);
+  const double b = p.b_store ? (double)b_decode(p.b_store, p.col_dt, col) : 1.0;
+  if (GLU) return h / (1.0 + exp(-h)) * ((double)b_decode(p.y, XDT, row * p.ld + col) * b);
+  return h * ((p.g ? (double)b_decode(p.g, XDT, col) : 1.0) * b) * rstd;
 }
 
-// The lane's codes (8 bytes, or 4 in cw[0]) and its group's scale to memory.
+// A block scale to memory.
 template <int FMT>
-__device__ __forceinline__ void store8(const RowProblem& p, int64_t row, int64_t col, const uint32_t* cw, float a, bool bad) {
-  constexpr int LG = group_lanes(FMT);
-  const int64_t at = row * p.K + col;
-  if (FMT == FMT_MXFP8)
-    *reinterpret_cast<uint2*>(p.codes + at) = make_uint2(cw[0], cw[1]);
+__device__ __forceinline__ void store_scale(const RowProblem& p, int64_t row, int64_t group, float a, bool bad) {
+  unsigned char* s = p.scales + row * p.nb + group;
+  if (bad)
+    *s = fmt_pow2(FMT) ? 0xFFu : 0x7Fu;
   else
-    *reinterpret_cast<uint32_t*>(p.codes + (at >> 1)) = cw[0];
-  if ((threadIdx.x & (LG - 1)) == 0) {
-    unsigned char* s = p.scales + row * p.nb + col / (8 * LG);
-    if (bad)
-      *s = fmt_pow2(FMT) ? 0xFFu : 0x7Fu;
-    else
-      a_store_f<FMT>(s, 0, a);
-  }
+    a_store_f<FMT>(s, 0, a);
 }
 
-// A warp's 32 x 8 elements decided in fp64 throughout and stored: the cold path,
-// out of line.  A group with a value that is not finite in fp32 gets the
-// format's NaN scale and zero codes; returns whether the lane's group did.
+// One group decided in fp64 and stored, an element a lane: the cold path, out
+// of line.  Every lane of the warp calls it with the same arguments.  A group
+// with a value that is not finite in fp32 gets the format's NaN scale and zero
+// codes; returns whether it did.
 template <int FMT, int XDT, bool GLU>
-static __device__ __noinline__ bool quant_exact(const RowProblem& p, int64_t row, int64_t col, bool on, double rstd, float sT) {
-  constexpr int LG = group_lanes(FMT);
-  double x[8], m = 0.0;
-  if (on) {
-    exact8<XDT, GLU>(p, row, col, rstd, x);
+static __device__ __noinline__ bool quant_exact(const RowProblem& p, int64_t row, int64_t col, double rstd, float sT) {
+  constexpr int G = FMT == FMT_NVFP4 ? 16 : 32;
+  const int lane = threadIdx.x & 31;
+  const double x = lane < G ? exact1<XDT, GLU>(p, row, col + lane, rstd) : 0.0;
+  double m = fabs(x) <= (double)kFltMax ? fabs(x) : CUDART_INF;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmax(m, fabs(x[i]) <= (double)kFltMax ? fabs(x[i]) : CUDART_INF);
-  }
-#pragma unroll
-  for (int o = 1; o < LG; o <<= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (!on) return false;
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
   const bool bad = m > (double)kFltMax;
   const float a = m == 0.0 || bad ? 1.f : (float)a_project<FMT>(m / grid_qmax(FMT), (double)sT);
-  uint32_t cw[2] = {0u, 0u};
-  if (!bad) codes_exact<FMT>(x, FMT == FMT_NVFP4 ? (double)sT * (double)a : (double)a, cw);
-  store8<FMT>(p, row, col, cw, a, bad);
+  uint32_t c = bad ? 0u : mag_code<FMT>(fabs(x), FMT == FMT_NVFP4 ? (double)sT * (double)a : (double)a);
+  if (c != 0 && x < 0.0) c |= FMT == FMT_MXFP8 ? 0x80u : 8u;
+  const int64_t at = row * p.K + col + lane;
+  if (FMT == FMT_MXFP8) {
+    p.codes[at] = (unsigned char)c;
+  } else {
+    const uint32_t high = __shfl_down_sync(0xffffffffu, c, 1);
+    if (lane < G && (lane & 1) == 0) p.codes[at >> 1] = (unsigned char)(c | (high << 4));
+  }
+  if (lane == 0) store_scale<FMT>(p, row, col / G, a, bad);
   return bad;
 }
 
-// Quantizes and stores the 8 elements of a lane at (row, col).  v: fp32 values
-// of x' known to a relative delta/2.  `force` sends the warp to fp64.  Every
-// lane of the warp calls it; `on` lanes hold data, the others zeros.  One
-// undecided lane sends the whole warp to fp64 (about one call in 100 at most):
-// zeros go there too, as their scale is 1 only if no product underflowed.
-template <int FMT, int XDT, bool GLU>
-__device__ __forceinline__ bool quant_store8(const RowProblem& p, int64_t row, int64_t col, bool on, const f2* v, float delta,
-                                             float sT, float isT, bool force, double rstd) {
-  constexpr int LG = group_lanes(FMT);
-  float m = 0.f;
+__device__ __forceinline__ float absmax16(const f2* v) {
+  float m = max_nan(fabsf(lo_of(v[0])), fabsf(hi_of(v[0])));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max3_nan(m, fabsf(lo_of(v[i])), fabsf(hi_of(v[i])));
+  for (int i = 1; i < 8; ++i) m = max3_nan(m, fabsf(lo_of(v[i])), fabsf(hi_of(v[i])));
+  return m;
+}
+
+// Quantizes and stores the 16 elements of a lane at (row, col).  v: fp32 values
+// of x' whose relative error, with the rounding of the scaled value, is below
+// delta.  `zero`: the lane's x' are zeros for certain (an fp32 zero alone may be
+// an underflow).  `force` sends the lane's group to fp64.  Every lane of the
+// warp calls it; `on` lanes hold data, the others zeros.  A group with an
+// undecided lane is decided in fp64 by the whole warp, an element a lane (about
+// one group in 1500; done by its own lanes, one element after the other, it took
+// 5 us).  Returns whether one of the warp's groups is not finite.
+template <int FMT, int XDT, bool GLU>
+__device__ __forceinline__ bool quant_store16(const RowProblem& p, int64_t row, int64_t col, bool on, const f2* v, float delta,
+                                              float sT, float isT, bool zero, bool force, double rstd) {
+  constexpr int LG = group_lanes(FMT), CW = code_words(FMT);
+  float m = absmax16(v);
 #pragma unroll
   for (int o = 1; o < LG; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  bool redo = force;
-  const float a = a_fast<FMT>(m, (float)grid_qmax(FMT), isT, redo);  // flags a NaN or an infinity too
+  bool redo = false;
+  float a = a_fast<FMT>(m, (float)grid_qmax(FMT), isT, redo);  // flags a zero, a NaN or an infinity too
   const float ia = fmt_pow2(FMT) ? __uint_as_float(0x7F000000u - __float_as_uint(a)) : __frcp_rn(a);
   const float c = FMT == FMT_NVFP4 ? isT * ia : ia;
-  uint32_t cw[2], cl[2];
+  uint32_t cw[CW], cl[CW], differ = 0;
   codes_fast<FMT>(v, c * (1.f - delta), cl);
   codes_fast<FMT>(v, c * (1.f + delta), cw);
-  redo |= cl[0] != cw[0] || cl[1] != cw[1];
-  if (__any_sync(0xffffffffu, redo && on)) return quant_exact<FMT, XDT, GLU>(p, row, col, on, rstd, sT);
-  if (on) {
-    cw[0] = no_negzero<FMT>(cw[0]);
-    if (FMT == FMT_MXFP8) cw[1] = no_negzero<FMT>(cw[1]);
-    store8<FMT>(p, row, col, cw, a, false);
+#pragma unroll
+  for (int w = 0; w < CW; ++w) differ |= cl[w] ^ cw[w];
+  if (m == 0.f) redo = !zero;  // a is 1 then; differ is 0
+  redo |= differ != 0 || force;
+  redo &= on;
+  const uint32_t lanes = __ballot_sync(0xffffffffu, redo);
+  const uint32_t groups = LG == 1 ? lanes : (lanes | (lanes >> 1)) & 0x55555555u;  // bit of a group's first lane
+  if (on && !(groups >> (threadIdx.x & 31 & ~(LG - 1)) & 1u)) {
+    const int64_t at = row * p.K + col;
+#pragma unroll
+    for (int w = 0; w < CW; ++w) cw[w] = no_negzero<FMT>(cw[w]);
+    if (FMT == FMT_MXFP8) {
+      if (p.codes_vec) {
+        *reinterpret_cast<uint4*>(p.codes + at) = make_uint4(cw[0], cw[1], cw[2 % CW], cw[3 % CW]);
+      } else {
+        *reinterpret_cast<uint2*>(p.codes + at) = make_uint2(cw[0], cw[1]);
+        *reinterpret_cast<uint2*>(p.codes + at + 8) = make_uint2(cw[2 % CW], cw[3 % CW]);
+      }
+    } else {
+      *reinterpret_cast<uint2*>(p.codes + (at >> 1)) = make_uint2(cw[0], cw[1]);
+    }
+    if ((threadIdx.x & (LG - 1)) == 0) store_scale<FMT>(p, row, col / (16 * LG), a, false);
   }
-  return false;
+  bool bad = false;
+  for (uint32_t rest = groups; rest != 0; rest &= rest - 1)
+    bad |= quant_exact<FMT, XDT, GLU>(p, row, __shfl_sync(0xffffffffu, col, __ffs(rest) - 1), rstd, sT);
+  return bad;
 }
 
 // Grid-wide barrier of a cooperative launch (bounded wait).
@@ -301,32 +358,23 @@ __device__ __forceinline__ void amax_to_header(WsHeader* hdr, double amax) {
 }
 
 // ---------------------------------------------------------------------------
-// dq_norm_quant: a CTA takes rows grid-stride, thread t the 8-element chunks
-// t, t + blockDim, ...  With NC = 1, 2 or 4 a thread has at most NC chunks and
-// keeps its part of the row in registers; with NC = 1 and 2 it also reads the
-// next row while it works on this one, and with NC = 1 it keeps g b.  NC = 0
-// is for rows longer than 4 x 1024 chunks: the stored row is read again after
-// the sum.  The sum of squares is held in fp64.
+// dq_norm_quant: a CTA takes rows grid-stride, thread t the 16-element chunks
+// t, t + blockDim, ...  With NC > 0 a thread has at most NC chunks and keeps its
+// part of the row in registers; with NC = 0 (rows longer than 8 x 256 chunks)
+// the stored row is read again after the sum.  The sum of squares is held in
+// fp64.
 
 template <int XDT>
-__device__ __forceinline__ void gb8(const RowProblem& p, int64_t col, float* gb) {
-  b8_values(p, col, gb);
+__device__ __forceinline__ void gb16(const RowProblem& p, int64_t col, f2* gb) {
+  b16_values(p, col, gb);
   if (p.g) {
-    float g[8];
-    h8_values<XDT>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.g) + col)), g);
+    f2 g[8];
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.g) + col);
+    const uint4 v0 = __ldg(q), v1 = __ldg(q + 1);
+    pairs16<XDT>(V16{{v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w}}, g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) gb[i] *= g[i];  // exact: at most 22 significant bits
+    for (int i = 0; i < 8; ++i) gb[i] = mul2(gb[i], g[i]);  // exact: at most 22 significant bits
   }
-}
-
-__device__ __forceinline__ uint4 load16(const void* base, int64_t off) {
-  return *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + off);
-}
-
-// h = x + r, rounded to the input type.
-template <int XDT>
-__device__ __forceinline__ uint4 add8(const uint4& x, const uint4& r) {
-  return make_uint4(h2_add<XDT>(x.x, r.x), h2_add<XDT>(x.y, r.y), h2_add<XDT>(x.z, r.z), h2_add<XDT>(x.w, r.w));
 }
 
 // 1/rms of the row from the threads' partial sums of squares; NaN for a row
@@ -350,53 +398,55 @@ __device__ __forceinline__ double row_rstd(double s, double* red, const RowProbl
   return red[32];
 }
 
-// Largest finite |x'| of a lane's 8 elements, in fp64.
+// Raises amax to the largest finite |x'| of the 512 elements whose lanes ask for
+// it, in fp64, an element a lane; every lane of the warp calls it.
 template <int XDT, bool GLU>
-static __device__ __noinline__ double amax_exact(const RowProblem& p, int64_t row, int64_t col, double rstd) {
-  double x[8], m = 0.0;
-  exact8<XDT, GLU>(p, row, col, rstd, x);
+static __device__ __noinline__ double amax_exact(const RowProblem& p, int64_t row, int64_t col, uint32_t lanes, double rstd,
+                                                 double amax) {
+  const int lane = threadIdx.x & 31;
+  for (uint32_t rest = lanes; rest != 0; rest &= rest - 1) {
+    const int64_t c0 = __shfl_sync(0xffffffffu, col, __ffs(rest) - 1);
+    const double x = lane < 16 ? fabs(exact1<XDT, GLU>(p, row, c0 + lane, rstd)) : 0.0;
+    if (x <= (double)kFltMax) amax = fmax(amax, x);
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (fabs(x[i]) <= (double)kFltMax) m = fmax(m, fabs(x[i]));
-  return m;
+  for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  return amax;
 }
 
+// Lanes whose fp32 maximum m (a relative 2^-20 off) could raise the warp's amax.
+// Of those, only the ones next to the largest m of them.
+__device__ __forceinline__ uint32_t amax_lanes(float m, bool on, bool force, double amax) {
+  const bool could = on && (force || !((double)m * (1.0 + 0x1p-18) < amax) || (m < 0x1p-60f && amax < 0x1p-59));
+  if (!__any_sync(0xffffffffu, could)) return 0;
+  // a NaN, an infinity or a tiny value says nothing about the others
+  const bool plain = could && !force && m >= 0x1p-60f && m <= kFltMax;
+  float top = plain ? m : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return __ballot_sync(0xffffffffu, could && !(plain && m * (1.f + 0x1p-18f) < top));
+}
+
+__host__ __device__ constexpr int norm_threads(int nc) { return nc == 1 ? 512 : 256; }
+
 template <int FMT, int XDT, int NC>
-__global__ void __launch_bounds__(NC == 1 || NC == 2 ? 512 : 1024, NC == 1 || NC == 2 ? 2 : 1)
-    k_norm(const __grid_constant__ RowProblem p) {
+__global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(const __grid_constant__ RowProblem p) {
   __shared__ double red[33];
   constexpr int N = NC > 0 ? NC : 1;
-  constexpr bool AHEAD = NC == 1 || NC == 2, KEEP = NC == 1;
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int chunks = (int)(p.K / 8);
+  const int chunks = (int)(p.K / 16);
   const int trips = NC > 0 ? 1 : (chunks + nt - 1) / nt;
   const void* hsrc = p.y ? p.h : p.x;
-  float gb[N][8];
-  auto get_gb = [&](int c, int ch) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) gb[c][i] = 0.f;
-    if (ch < chunks) gb8<XDT>(p, ch * 8, gb[c]);
-  };
-  uint4 xv[N], rv[N];  // the next row's inputs
-  auto read = [&](int64_t row) {
-#pragma unroll
-    for (int c = 0; c < N; ++c) {
-      const int ch = tid + c * nt;
-      xv[c] = rv[c] = make_uint4(0, 0, 0, 0);
-      if (row < p.M && ch < chunks) {
-        xv[c] = load16(p.x, row * p.K + ch * 8);
-        if (p.y) rv[c] = load16(p.y, row * p.K + ch * 8);
-      }
-    }
-  };
-  if (AHEAD) {
-    read(blockIdx.x);
-    if (KEEP) get_gb(0, tid);
-  }
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
-  uint4 hv[N];
+  V16 hv[N];
+  f2 gb1[NC == 1 ? 8 : 1];  // a thread's only chunk: its g b, read while the row is on its way
+  if (NC == 1) {
+#pragma unroll
+    for (int i = 0; i < (NC == 1 ? 8 : 1); ++i) gb1[i] = 0ull;
+    if (tid < chunks) gb16<XDT>(p, tid * 16, gb1);
+  }
   // pass 0 (NVFP4): sums, 1/rms and the tensor's amax; pass 1: scales and codes
 #pragma unroll 1
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
@@ -418,30 +468,33 @@ __global__ void __launch_bounds__(NC == 1 || NC == 2 ? 512 : 1024, NC == 1 || NC
 #pragma unroll
           for (int c = 0; c < N; ++c) {
             const int ch = tid + (NC > 0 ? c : t) * nt;
-            if (!AHEAD) {
-              xv[c] = rv[c] = make_uint4(0, 0, 0, 0);
-              if (ch < chunks) {
-                xv[c] = load16(p.x, row * p.K + ch * 8);
-                if (p.y) rv[c] = load16(p.y, row * p.K + ch * 8);
-              }
+            hv[c] = ch < chunks ? load16(p.x, row * p.K + ch * 16, p.wide) : zero16();
+          }
+          if (p.y) {
+            V16 r[N];
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+              const int ch = tid + (NC > 0 ? c : t) * nt;
+              r[c] = ch < chunks ? load16(p.y, row * p.K + ch * 16, p.wide) : zero16();
+            }
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+              const int ch = tid + (NC > 0 ? c : t) * nt;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) hv[c].u[i] = h2_add<XDT>(hv[c].u[i], r[c].u[i]);
+              if (ch < chunks) store16(p.h, row * p.K + ch * 16, p.wide, hv[c]);
             }
           }
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            const int ch = tid + (NC > 0 ? c : t) * nt;
-            hv[c] = xv[c];
-            if (p.y) {
-              hv[c] = add8<XDT>(xv[c], rv[c]);
-              if (ch < chunks)
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.h) + row * p.K + ch * 8) = hv[c];
-            }
-            float h[8];
-            h8_values<XDT>(hv[c], h);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s = fma((double)h[i], (double)h[i], s);
+            for (int i = 0; i < 8; ++i) {
+              const float2 h = h2_values(hv[c].u[i], XDT);
+              s = fma((double)h.x, (double)h.x, s);
+              s = fma((double)h.y, (double)h.y, s);
+            }
           }
         }
-        if (AHEAD) read(row + gridDim.x);
         rstd = row_rstd(s, red, p);
         if (FMT == FMT_NVFP4 && tid == 0) p.rstd[row] = rstd;
       } else {
@@ -455,73 +508,112 @@ __global__ void __launch_bounds__(NC == 1 || NC == 2 ? 512 : 1024, NC == 1 || NC
         for (int c = 0; c < N; ++c) {
           const int ch = tid + (NC > 0 ? c : t) * nt;
           const bool on = ch < chunks;
-          if (NC == 0 || (FMT == FMT_NVFP4 && pass == 1))
-            hv[c] = on ? load16(hsrc, row * p.K + ch * 8) : make_uint4(0, 0, 0, 0);
-          if (!KEEP) get_gb(c, ch);
-          float h[8];
-          h8_values<XDT>(hv[c], h);
-          f2 v[4];
+          if (NC > 1 && (tid & ~31) + c * nt >= chunks) break;  // the whole warp is past the row
+          if (NC == 0 || (FMT == FMT_NVFP4 && pass == 1)) hv[c] = on ? load16_again(hsrc, row * p.K + ch * 16) : zero16();
+          f2 v[8], gb[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            v[i] = on ? mul2(mul2(pk(h[2 * i], h[2 * i + 1]), splat(rs)), pk(gb[c][2 * i], gb[c][2 * i + 1])) : 0ull;
+          for (int i = 0; i < 8; ++i) gb[i] = 0ull;
+          if (NC == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gb[i] = gb1[i];
+          } else if (on) {
+            gb16<XDT>(p, ch * 16, gb);
+          }
+          pairs16<XDT>(hv[c], v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = on ? mul2(mul2(v[i], splat(rs)), gb[i]) : 0ull;
           if (FMT == FMT_NVFP4 && pass == 0) {
             // values that are not finite have no share in the tensor scale
-            if (on && rstd == rstd) {
-              float mf = 0.f;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mf = max3_nan(mf, fabsf(lo_of(v[i])), fabsf(hi_of(v[i])));
-              // fp64 only where the fp32 value could raise the maximum
-              if (!((double)mf * (1.0 + 0x1p-18) < amax) || !rs_ok || (mf < 0x1p-60f && amax < 0x1p-59))
-                amax = fmax(amax, amax_exact<XDT, false>(p, row, ch * 8, rstd));
-            }
+            const float mf = absmax16(v);
+            const uint32_t ask = amax_lanes(mf, on && rstd == rstd, !rs_ok, amax);
+            if (ask) amax = amax_exact<XDT, false>(p, row, ch * 16, ask, rstd, amax);
           } else {
-            bad |= quant_store8<FMT, XDT, false>(p, row, ch * 8, on, v, 0x1p-20f, sT, isT, !sT_ok || !rs_ok, rstd);
+            // relative error: 1/rms, two products, the scale's factor and the scaled value, 2^-24 each (NVFP4: three more)
+            bad |= quant_store16<FMT, XDT, false>(p, row, ch * 16, on, v, 0x1p-20f, sT, isT, zero_bits16(hv[c]),
+                                                  !sT_ok || !rs_ok, rstd);
           }
         }
       }
     }
   }
   if (blockIdx.x == 0 && tid == 0 && p.sT_out) *p.sT_out = sT;
-  if (__any_sync(0xffffffffu, bad) && (tid & 31) == 0) atomicOr(&p.hdr->flags, kFlagNonFinite);
+  if (bad && (tid & 31) == 0) atomicOr(&p.hdr->flags, kFlagNonFinite);
 }
 
 // ---------------------------------------------------------------------------
 // dq_glu_quant: elementwise but for the groups, so the warps of the grid take
-// items of 32 x 8 consecutive columns of a row, row-major and grid-stride, and
-// read the next item while they work on one.
+// items of 32 x 16 consecutive columns of a row, row-major and grid-stride, and
+// read the next item while they work on one.  The grid's warps are a multiple
+// of a row's items where there are enough, so a warp keeps its columns and
+// their scales.
 
-// x' in fp32: relative error below 10 * 2^-24 (expf within 2 ulp, six further
-// roundings) while exp(-gate) and up * b stay in range; `far` marks the rest.
-// (An up * b below fp32's normal range gives |x'| < 2^-86 here: a zero code in
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Smallest and largest of a lane's 16-bit elements (NaN ignored).
+template <int XDT>
+__device__ __forceinline__ void range16(const V16& v, float& lo, float& hi) {
+  uint32_t a = v.u[0], b = v.u[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    if (XDT == DT_BF16) {
+      asm("min.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(v.u[i]));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(b) : "r"(v.u[i]));
+    } else {
+      asm("min.f16x2 %0, %0, %1;" : "+r"(a) : "r"(v.u[i]));
+      asm("max.f16x2 %0, %0, %1;" : "+r"(b) : "r"(v.u[i]));
+    }
+  }
+  const float2 x = h2_values(a, XDT), y = h2_values(b, XDT);
+  lo = fminf(x.x, x.y);
+  hi = fmaxf(y.x, y.y);
+}
+
+// x' in fp32.  exp(-g) = 2^t (1 + ln2 r) with t = fp32(-g log2 e) and r what its
+// rounding left out, formed by fma; ex2.approx is good to 2^-22.5, rcp.approx to
+// 2^-23, and five further roundings give 2^-21 in all.  `far` marks gates whose
+// exponential (below -80) or product with an underflowed up * b (above 2^40)
+// leaves that bound; an up * b that overflows shows as an infinity or a NaN.
+// (Otherwise an up * b below the normal range gives |x'| < 2^-86: a zero code in
 // every group whose scale the fast path settles.)
 template <int XDT>
-__device__ __forceinline__ void glu_fast8(const uint4& gv, const uint4& uv, const float* b, f2* v, bool& far) {
-  float g[8], u[8];
-  h8_values<XDT>(gv, g);
-  h8_values<XDT>(uv, u);
+__device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const f2* b, f2* v, bool& far) {
+  float lo, hi;
+  range16<XDT>(gv, lo, hi);
+  far = !(lo >= -80.f && hi <= 0x1p40f);
+  f2 g[8], u[8];
+  pairs16<XDT>(gv, g);
+  pairs16<XDT>(uv, u);
+  // -log2(e) as the sum of two fp32 numbers
+  const f2 l1 = splat(-1.44269502f), l2 = splat((float)(-1.4426950408889634 + (double)1.44269502f));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float r[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float gg = g[2 * i + k], ub = u[2 * i + k] * b[2 * i + k];
-      far |= !(gg >= -80.f && gg <= 0x1p40f) || !(fabsf(ub) <= kFltMax);
-      r[k] = gg * __frcp_rn(1.f + expf(-gg)) * ub;
-    }
-    v[i] = pk(r[0], r[1]);
+  for (int i = 0; i < 8; ++i) {
+    const f2 t = mul2(g[i], l1);
+    const f2 r = fma2(g[i], l2, fma2(g[i], l1, mul2(t, splat(-1.f))));
+    f2 e = pk(ex2_approx(lo_of(t)), ex2_approx(hi_of(t)));
+    e = fma2(e, mul2(r, splat(0.693147181f)), e);
+    const f2 d = add2(e, splat(1.f));
+    const f2 s = pk(rcp_approx(lo_of(d)), rcp_approx(hi_of(d)));
+    v[i] = mul2(mul2(g[i], s), mul2(u[i], b[i]));
   }
 }
 
 template <int FMT, int XDT>
-__global__ void __launch_bounds__(kGluThreads, 4) k_glu(const __grid_constant__ RowProblem p) {
+__global__ void __launch_bounds__(kGluThreads, 3) k_glu(const __grid_constant__ RowProblem p) {
   const int lane = threadIdx.x & 31;
-  const int64_t spans = (p.K + 255) / 256;  // 256-column pieces of a row
+  const int64_t spans = (p.K + 511) / 512;  // 512-column pieces of a row
   const int64_t w0 = (int64_t)blockIdx.x * (kGluThreads / 32) + (threadIdx.x >> 5);
-  const int64_t nw = (int64_t)gridDim.x * (kGluThreads / 32);
-  const int64_t drow = nw / spans, dspan = nw - drow * spans;  // the grid's stride as rows and spans
+  const int64_t all = (int64_t)gridDim.x * (kGluThreads / 32);
+  const int64_t nw = all >= spans ? all / spans * spans : all;  // warps that take items
+  const int64_t drow = nw / spans, dspan = nw - drow * spans;   // the grid's stride as rows and spans
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
+  f2 b[8];
+  int64_t have = -1;
 #pragma unroll 1
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
     if (FMT == FMT_NVFP4 && pass == 1) {
@@ -532,22 +624,28 @@ __global__ void __launch_bounds__(kGluThreads, 4) k_glu(const __grid_constant__ 
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
-    int64_t row = w0 / spans, span = w0 - row * spans;
-    uint4 gn, un;
+    int64_t row = w0 < nw ? w0 / spans : p.M, span = w0 - row * spans;
+    V16 gn, un;
     auto read = [&]() {
-      const int64_t col = span * 256 + lane * 8;
-      gn = un = make_uint4(0, 0, 0, 0);
+      const int64_t col = span * 512 + lane * 16;
+      gn = un = zero16();
       if (row < p.M && col < p.K) {
-        gn = load16(p.x, row * p.ld + col);
-        un = load16(p.y, row * p.ld + col);
+        gn = load16(p.x, row * p.ld + col, p.wide);
+        un = load16(p.y, row * p.ld + col, p.wide);
       }
     };
     read();
 #pragma unroll 1
     while (row < p.M) {
-      const int64_t r = row, col = span * 256 + lane * 8;
+      const int64_t r = row, col = span * 512 + lane * 16;
       const bool on = col < p.K;
-      const uint4 gv = gn, uv = un;
+      const V16 gv = gn, uv = un;
+      if (span != have) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = 0ull;
+        if (on) b16_values(p, col, b);
+        have = span;
+      }
       row += drow;
       span += dspan;
       if (span >= spans) {
@@ -555,28 +653,22 @@ __global__ void __launch_bounds__(kGluThreads, 4) k_glu(const __grid_constant__ 
         ++row;
       }
       read();
-      float b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = 0.f;
-      if (on) b8_values(p, col, b);
-      f2 v[4];
-      bool far = false;
-      glu_fast8<XDT>(gv, uv, b, v, far);
+      f2 v[8];
+      bool far;
+      glu_fast16<XDT>(gv, uv, b, v, far);
       if (FMT == FMT_NVFP4 && pass == 0) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) m = max3_nan(m, fabsf(lo_of(v[i])), fabsf(hi_of(v[i])));
-        // fp64 only where the fp32 value could raise the maximum; values that
-        // are not finite have no share in it
-        if (on && (far || !((double)m * (1.0 + 0x1p-18) < amax) || (m < 0x1p-60f && amax < 0x1p-59)))
-          amax = fmax(amax, amax_exact<XDT, true>(p, r, col, 0.0));
+        // values that are not finite have no share in the tensor scale
+        const uint32_t ask = amax_lanes(absmax16(v), on, far, amax);
+        if (ask) amax = amax_exact<XDT, true>(p, r, col, ask, 0.0, amax);
       } else {
-        bad |= quant_store8<FMT, XDT, true>(p, r, col, on, v, 0x1p-19f, sT, isT, !sT_ok || far, 0.0);
+        // 2^-21 of x' and the roundings of the scaled value
+        bad |= quant_store16<FMT, XDT, true>(p, r, col, on, v, 1.25f * 0x1p-20f, sT, isT, zero_bits16(gv) || zero_bits16(uv),
+                                               !sT_ok || far, 0.0);
       }
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.sT_out) *p.sT_out = sT;
-  if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&p.hdr->flags, kFlagNonFinite);
+  if (bad && lane == 0) atomicOr(&p.hdr->flags, kFlagNonFinite);
 }
 
 // ---------------------------------------------------------------------------
@@ -600,22 +692,30 @@ static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, boo
   return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(threads), args, (size_t)0, st);
 }
 
+// Few rows: a chunk a thread, for latency.  From 4 rows an SM on: CTAs of two
+// warps or little more with up to 4 chunks a thread, which leave each other less
+// idle at the row's two barriers (8192 x 4096 MXFP8: 74 us with 1 chunk a
+// thread, 62 with 2, 58 with 4, 77 with 8, whose registers halve the warps).
 template <int FMT, int XDT>
 static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
-  const int64_t chunks = p.K / 8;
-  const int nc = chunks <= 512 ? 1 : (chunks <= 1024 ? 2 : (chunks <= 4096 ? 4 : 0));
-  const int64_t per = nc > 0 ? (chunks + nc - 1) / nc : 1024;
-  const int threads = (int)((per + 31) / 32 * 32);
+  const int64_t chunks = p.K / 16;
+  int nc, threads;
+  if (p.M >= 4 * (int64_t)sms)
+    nc = chunks <= 64 ? 1 : (chunks <= 128 ? 2 : (chunks <= 4 * 256 ? 4 : (chunks <= 8 * 256 ? 8 : 0)));
+  else
+    nc = chunks <= 512 ? 1 : (chunks <= 8 * 256 ? 8 : 0);
+  threads = nc == 0 ? 256 : (int)(((chunks + nc - 1) / nc + 31) / 32 * 32);
   void (*kern)(RowProblem) = nc == 1   ? k_norm<FMT, XDT, 1>
                              : nc == 2 ? k_norm<FMT, XDT, 2>
                              : nc == 4 ? k_norm<FMT, XDT, 4>
+                             : nc == 8 ? k_norm<FMT, XDT, 8>
                                        : k_norm<FMT, XDT, 0>;
   return row_launch(kern, p, FMT == FMT_NVFP4, p.M, threads, sms, st);
 }
 
 template <int FMT, int XDT>
 static cudaError_t glu_launch(const RowProblem& p, int sms, cudaStream_t st) {
-  const int64_t items = p.M * ((p.K + 255) / 256);
+  const int64_t items = p.M * ((p.K + 511) / 512);
   return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, sms, st);
 }
 
@@ -648,6 +748,7 @@ static void row_fill(RowProblem* p, int64_t rows, int64_t cols, const void* col_
   p->b_store = col_scales;
   p->col_dt = col_dtype;
   p->b_vec = col_scales != nullptr && (uintptr_t)col_scales % 16 == 0;
+  p->codes_vec = (uintptr_t)out->codes % 16 == 0;
   p->M = rows;
   p->K = cols;
   p->codes = static_cast<unsigned char*>(out->codes);
@@ -686,6 +787,7 @@ extern "C" int dq_norm_quant(const void* X, const void* residual, int x_dtype, i
   p.ld = cols;
   p.eps = eps;
   p.h = residual_out;
+  p.wide = ((uintptr_t)X | (uintptr_t)residual | (uintptr_t)residual_out) % 32 == 0;  // a row is a multiple of 32 bytes
   p.rstd = reinterpret_cast<double*>(static_cast<unsigned char*>(workspace) + DQ_ACT_WORKSPACE_BYTES);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(dq::WsHeader), s) != cudaSuccess) return DQ_ECUDA;
@@ -714,6 +816,7 @@ extern "C" int dq_glu_quant(const void* gate, const void* up, int x_dtype, int64
   p.x = gate;
   p.y = up;
   p.ld = ld;
+  p.wide = ((uintptr_t)gate | (uintptr_t)up | (uintptr_t)(2 * ld)) % 32 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(workspace, 0, sizeof(dq::WsHeader), s) != cudaSuccess) return DQ_ECUDA;
   cudaError_t e;
