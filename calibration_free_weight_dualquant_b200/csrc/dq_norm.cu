@@ -48,7 +48,6 @@ struct RowProblem {
   void* h;                // residual sum out (aliases x or y at will) or NULL
   unsigned char* codes;
   unsigned char* scales;  // [M][nb] bytes
-  int64_t nb;
   float* sT_out;
   double* rstd;           // NVFP4 norm: 1/rms of every row between the passes
   WsHeader* hdr;
@@ -233,24 +232,25 @@ __device__ __forceinline__ double exact1(const RowProblem& p, int64_t row, int64
   return h * ((p.g ? (double)b_decode(p.g, XDT, col) : 1.0) * b) * rstd;
 }
 
-// A block scale to memory.
+// The scale of the block that holds element `at` (row * K + column) to memory.
 template <int FMT>
-__device__ __forceinline__ void store_scale(const RowProblem& p, int64_t row, int64_t group, float a, bool bad) {
-  unsigned char* s = p.scales + row * p.nb + group;
+__device__ __forceinline__ void store_scale(const RowProblem& p, int64_t at, float a, bool bad) {
+  unsigned char* s = p.scales + (at >> (FMT == FMT_NVFP4 ? 4 : 5));  // a row is a whole number of groups
   if (bad)
     *s = fmt_pow2(FMT) ? 0xFFu : 0x7Fu;
   else
     a_store_f<FMT>(s, 0, a);
 }
 
-// One group decided in fp64 and stored, an element a lane: the cold path, out
-// of line.  Every lane of the warp calls it with the same arguments.  A group
+// The group from element `first` decided in fp64 and stored, an element a lane:
+// the cold path, out of line.  Every lane of the warp calls it with the same arguments.  A group
 // with a value that is not finite in fp32 gets the format's NaN scale and zero
 // codes; returns whether it did.
 template <int FMT, int XDT, bool GLU>
-static __device__ __noinline__ bool quant_exact(const RowProblem& p, int64_t row, int64_t col, double rstd, float sT) {
+static __device__ __noinline__ bool quant_exact(const RowProblem& p, int64_t first, double rstd, float sT) {
   constexpr int G = FMT == FMT_NVFP4 ? 16 : 32;
   const int lane = threadIdx.x & 31;
+  const int64_t row = first / p.K, col = first - row * p.K;
   const double x = lane < G ? exact1<XDT, GLU>(p, row, col + lane, rstd) : 0.0;
   double m = fabs(x) <= (double)kFltMax ? fabs(x) : CUDART_INF;
 #pragma unroll
@@ -259,14 +259,14 @@ static __device__ __noinline__ bool quant_exact(const RowProblem& p, int64_t row
   const float a = m == 0.0 || bad ? 1.f : (float)a_project<FMT>(m / grid_qmax(FMT), (double)sT);
   uint32_t c = bad ? 0u : mag_code<FMT>(fabs(x), FMT == FMT_NVFP4 ? (double)sT * (double)a : (double)a);
   if (c != 0 && x < 0.0) c |= FMT == FMT_MXFP8 ? 0x80u : 8u;
-  const int64_t at = row * p.K + col + lane;
+  const int64_t at = first + lane;
   if (FMT == FMT_MXFP8) {
     p.codes[at] = (unsigned char)c;
   } else {
     const uint32_t high = __shfl_down_sync(0xffffffffu, c, 1);
     if (lane < G && (lane & 1) == 0) p.codes[at >> 1] = (unsigned char)(c | (high << 4));
   }
-  if (lane == 0) store_scale<FMT>(p, row, col / G, a, bad);
+  if (lane == 0) store_scale<FMT>(p, first, a, bad);
   return bad;
 }
 
@@ -277,17 +277,17 @@ __device__ __forceinline__ float absmax16(const f2* v) {
   return m;
 }
 
-// Quantizes and stores the 16 elements of a lane at (row, col).  v: fp32 values
-// of x' whose relative error, with the rounding of the scaled value, is below
-// delta.  `zero`: the lane's x' are zeros for certain (an fp32 zero alone may be
-// an underflow).  `force` sends the lane's group to fp64.  Every lane of the
+// Quantizes and stores the 16 elements of a lane from element `at`.  v: fp32
+// values of x' whose relative error, with the rounding of the scaled value, is
+// below delta.  zero(): the lane's x' are zeros for certain (an fp32 zero alone
+// may be an underflow).  `force` sends the lane's group to fp64.  Every lane of the
 // warp calls it; `on` lanes hold data, the others zeros.  A group with an
 // undecided lane is decided in fp64 by the whole warp, an element a lane (about
 // one group in 1500; done by its own lanes, one element after the other, it took
 // 5 us).  Returns whether one of the warp's groups is not finite.
-template <int FMT, int XDT, bool GLU>
-__device__ __forceinline__ bool quant_store16(const RowProblem& p, int64_t row, int64_t col, bool on, const f2* v, float delta,
-                                              float sT, float isT, bool zero, bool force, double rstd) {
+template <int FMT, int XDT, bool GLU, class Zero>
+__device__ __forceinline__ bool quant_store16(const RowProblem& p, int64_t at, bool on, const f2* v, float delta, float sT,
+                                              float isT, Zero&& zero, bool force, double rstd) {
   constexpr int LG = group_lanes(FMT), CW = code_words(FMT);
   float m = absmax16(v);
 #pragma unroll
@@ -301,13 +301,12 @@ __device__ __forceinline__ bool quant_store16(const RowProblem& p, int64_t row, 
   codes_fast<FMT>(v, c * (1.f + delta), cw);
 #pragma unroll
   for (int w = 0; w < CW; ++w) differ |= cl[w] ^ cw[w];
-  if (m == 0.f) redo = !zero;  // a is 1 then; differ is 0
+  if (m == 0.f) redo = !zero();  // a is 1 then; differ is 0
   redo |= differ != 0 || force;
   redo &= on;
   const uint32_t lanes = __ballot_sync(0xffffffffu, redo);
   const uint32_t groups = LG == 1 ? lanes : (lanes | (lanes >> 1)) & 0x55555555u;  // bit of a group's first lane
   if (on && !(groups >> (threadIdx.x & 31 & ~(LG - 1)) & 1u)) {
-    const int64_t at = row * p.K + col;
 #pragma unroll
     for (int w = 0; w < CW; ++w) cw[w] = no_negzero<FMT>(cw[w]);
     if (FMT == FMT_MXFP8) {
@@ -320,11 +319,11 @@ __device__ __forceinline__ bool quant_store16(const RowProblem& p, int64_t row, 
     } else {
       *reinterpret_cast<uint2*>(p.codes + (at >> 1)) = make_uint2(cw[0], cw[1]);
     }
-    if ((threadIdx.x & (LG - 1)) == 0) store_scale<FMT>(p, row, col / (16 * LG), a, false);
+    if ((threadIdx.x & (LG - 1)) == 0) store_scale<FMT>(p, at, a, false);
   }
   bool bad = false;
   for (uint32_t rest = groups; rest != 0; rest &= rest - 1)
-    bad |= quant_exact<FMT, XDT, GLU>(p, row, __shfl_sync(0xffffffffu, col, __ffs(rest) - 1), rstd, sT);
+    bad |= quant_exact<FMT, XDT, GLU>(p, __shfl_sync(0xffffffffu, at, __ffs(rest) - 1), rstd, sT);
   return bad;
 }
 
@@ -401,12 +400,11 @@ __device__ __forceinline__ double row_rstd(double s, double* red, const RowProbl
 // Raises amax to the largest finite |x'| of the 512 elements whose lanes ask for
 // it, in fp64, an element a lane; every lane of the warp calls it.
 template <int XDT, bool GLU>
-static __device__ __noinline__ double amax_exact(const RowProblem& p, int64_t row, int64_t col, uint32_t lanes, double rstd,
-                                                 double amax) {
+static __device__ __noinline__ double amax_exact(const RowProblem& p, int64_t at, uint32_t lanes, double rstd, double amax) {
   const int lane = threadIdx.x & 31;
   for (uint32_t rest = lanes; rest != 0; rest &= rest - 1) {
-    const int64_t c0 = __shfl_sync(0xffffffffu, col, __ffs(rest) - 1);
-    const double x = lane < 16 ? fabs(exact1<XDT, GLU>(p, row, c0 + lane, rstd)) : 0.0;
+    const int64_t first = __shfl_sync(0xffffffffu, at, __ffs(rest) - 1), row = first / p.K;
+    const double x = lane < 16 ? fabs(exact1<XDT, GLU>(p, row, first - row * p.K + lane, rstd)) : 0.0;
     if (x <= (double)kFltMax) amax = fmax(amax, x);
   }
 #pragma unroll
@@ -432,6 +430,8 @@ __host__ __device__ constexpr int norm_threads(int nc) { return nc == 1 ? 512 : 
 template <int FMT, int XDT, int NC>
 __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(const __grid_constant__ RowProblem p) {
   __shared__ double red[33];
+  // g b of the thread's own chunks (NC > 1), 16-byte pieces [c][piece][thread]: written and read by one thread
+  extern __shared__ uint4 gb_kept[];
   constexpr int N = NC > 0 ? NC : 1;
   const int tid = threadIdx.x, nt = blockDim.x;
   const int chunks = (int)(p.K / 16);
@@ -440,12 +440,28 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
-  V16 hv[N];
-  f2 gb1[NC == 1 ? 8 : 1];  // a thread's only chunk: its g b, read while the row is on its way
-  if (NC == 1) {
+  V16 hv[N], rv[N];  // zeros for good where the thread has no chunk
 #pragma unroll
-    for (int i = 0; i < (NC == 1 ? 8 : 1); ++i) gb1[i] = 0ull;
-    if (tid < chunks) gb16<XDT>(p, tid * 16, gb1);
+  for (int c = 0; c < N; ++c) hv[c] = rv[c] = zero16();
+  f2 gb[8];
+  auto get_gb = [&](int ch) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gb[i] = 0ull;
+    if (ch < chunks) gb16<XDT>(p, ch * 16, gb);
+  };
+  if (NC == 1) get_gb(tid);
+  if (NC > 1) {
+#pragma unroll 1
+    for (int c = 0; c < N; ++c) {
+      get_gb(tid + c * nt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ulonglong2 q;
+        q.x = gb[2 * i];
+        q.y = gb[2 * i + 1];
+        *reinterpret_cast<ulonglong2*>(&gb_kept[(c * 4 + i) * nt + tid]) = q;
+      }
+    }
   }
   // pass 0 (NVFP4): sums, 1/rms and the tensor's amax; pass 1: scales and codes
 #pragma unroll 1
@@ -458,8 +474,9 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
+    int64_t row0 = blockIdx.x * p.K + tid * 16;  // element of the thread's first chunk
 #pragma unroll 1
-    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+    for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, row0 += gridDim.x * p.K) {
       double rstd;
       if (FMT != FMT_NVFP4 || pass == 0) {
         double s = 0.0;
@@ -467,22 +484,20 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
         for (int t = 0; t < trips; ++t) {
 #pragma unroll
           for (int c = 0; c < N; ++c) {
-            const int ch = tid + (NC > 0 ? c : t) * nt;
-            hv[c] = ch < chunks ? load16(p.x, row * p.K + ch * 16, p.wide) : zero16();
+            const int i = (NC > 0 ? c : t) * nt;
+            if (NC == 0) hv[c] = rv[c] = zero16();
+            if (tid + i < chunks) {
+              hv[c] = load16(p.x, row0 + i * 16, p.wide);
+              if (p.y) rv[c] = load16(p.y, row0 + i * 16, p.wide);
+            }
           }
           if (p.y) {
-            V16 r[N];
 #pragma unroll
             for (int c = 0; c < N; ++c) {
-              const int ch = tid + (NC > 0 ? c : t) * nt;
-              r[c] = ch < chunks ? load16(p.y, row * p.K + ch * 16, p.wide) : zero16();
-            }
+              const int i = (NC > 0 ? c : t) * nt;
 #pragma unroll
-            for (int c = 0; c < N; ++c) {
-              const int ch = tid + (NC > 0 ? c : t) * nt;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) hv[c].u[i] = h2_add<XDT>(hv[c].u[i], r[c].u[i]);
-              if (ch < chunks) store16(p.h, row * p.K + ch * 16, p.wide, hv[c]);
+              for (int k = 0; k < 8; ++k) hv[c].u[k] = h2_add<XDT>(hv[c].u[k], rv[c].u[k]);
+              if (tid + i < chunks) store16(p.h, row0 + i * 16, p.wide, hv[c]);
             }
           }
 #pragma unroll
@@ -506,30 +521,31 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
       for (int t = 0; t < trips; ++t) {
 #pragma unroll
         for (int c = 0; c < N; ++c) {
-          const int ch = tid + (NC > 0 ? c : t) * nt;
-          const bool on = ch < chunks;
-          if (NC > 1 && (tid & ~31) + c * nt >= chunks) break;  // the whole warp is past the row
-          if (NC == 0 || (FMT == FMT_NVFP4 && pass == 1)) hv[c] = on ? load16_again(hsrc, row * p.K + ch * 16) : zero16();
-          f2 v[8], gb[8];
+          const int i0 = (NC > 0 ? c : t) * nt;
+          const bool on = tid + i0 < chunks;
+          if (NC > 1 && (tid & ~31) + i0 >= chunks) break;  // the whole warp is past the row
+          if (NC == 0 || (FMT == FMT_NVFP4 && pass == 1)) hv[c] = on ? load16_again(hsrc, row0 + i0 * 16) : zero16();
+          if (NC == 0) get_gb(tid + i0);
+          if (NC > 1) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) gb[i] = 0ull;
-          if (NC == 1) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) gb[i] = gb1[i];
-          } else if (on) {
-            gb16<XDT>(p, ch * 16, gb);
+            for (int i = 0; i < 4; ++i) {
+              const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&gb_kept[(c * 4 + i) * nt + tid]);
+              gb[2 * i] = q.x;
+              gb[2 * i + 1] = q.y;
+            }
           }
+          f2 v[8];
           pairs16<XDT>(hv[c], v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = on ? mul2(mul2(v[i], splat(rs)), gb[i]) : 0ull;
+          for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], splat(rs)), gb[i]);
           if (FMT == FMT_NVFP4 && pass == 0) {
             // values that are not finite have no share in the tensor scale
             const float mf = absmax16(v);
             const uint32_t ask = amax_lanes(mf, on && rstd == rstd, !rs_ok, amax);
-            if (ask) amax = amax_exact<XDT, false>(p, row, ch * 16, ask, rstd, amax);
+            if (ask) amax = amax_exact<XDT, false>(p, row0 + i0 * 16, ask, rstd, amax);
           } else {
             // relative error: 1/rms, two products, the scale's factor and the scaled value, 2^-24 each (NVFP4: three more)
-            bad |= quant_store16<FMT, XDT, false>(p, row, ch * 16, on, v, 0x1p-20f, sT, isT, zero_bits16(hv[c]),
+            bad |= quant_store16<FMT, XDT, false>(p, row0 + i0 * 16, on, v, 0x1p-20f, sT, isT, [&] { return zero_bits16(hv[c]); },
                                                   !sT_ok || !rs_ok, rstd);
           }
         }
@@ -587,14 +603,14 @@ __device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const f
   f2 g[8], u[8];
   pairs16<XDT>(gv, g);
   pairs16<XDT>(uv, u);
-  // -log2(e) as the sum of two fp32 numbers
-  const f2 l1 = splat(-1.44269502f), l2 = splat((float)(-1.4426950408889634 + (double)1.44269502f));
+  // log2(e) as the sum of two fp32 numbers
+  const f2 l1 = splat(1.44269502f), m1 = splat(-1.44269502f), l2 = splat((float)(1.4426950408889634 - (double)1.44269502f));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const f2 t = mul2(g[i], l1);
-    const f2 r = fma2(g[i], l2, fma2(g[i], l1, mul2(t, splat(-1.f))));
+    const f2 t = mul2(g[i], m1);
+    const f2 r = fma2(g[i], l2, fma2(g[i], l1, t));  // minus what t lacks
     f2 e = pk(ex2_approx(lo_of(t)), ex2_approx(hi_of(t)));
-    e = fma2(e, mul2(r, splat(0.693147181f)), e);
+    e = fma2(e, mul2(r, splat(-0.693147181f)), e);
     const f2 d = add2(e, splat(1.f));
     const f2 s = pk(rcp_approx(lo_of(d)), rcp_approx(hi_of(d)));
     v[i] = mul2(mul2(g[i], s), mul2(u[i], b[i]));
@@ -608,12 +624,15 @@ __global__ void __launch_bounds__(kGluThreads, 3) k_glu(const __grid_constant__ 
   const int64_t w0 = (int64_t)blockIdx.x * (kGluThreads / 32) + (threadIdx.x >> 5);
   const int64_t all = (int64_t)gridDim.x * (kGluThreads / 32);
   const int64_t nw = all >= spans ? all / spans * spans : all;  // warps that take items
-  const int64_t drow = nw / spans, dspan = nw - drow * spans;   // the grid's stride as rows and spans
+  const int drow = (int)(nw / spans), dspan = (int)(nw - drow * spans);  // the grid's stride as rows and spans
+  // ... and as elements of the inputs and outputs, without and with a carry into the next row
+  const int64_t din = drow * p.ld + dspan * 512, dout = drow * p.K + dspan * 512;
+  const int64_t cin = p.ld - spans * 512, cout = p.K - spans * 512;
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
   f2 b[8];
-  int64_t have = -1;
+  int have = -1;
 #pragma unroll 1
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
     if (FMT == FMT_NVFP4 && pass == 1) {
@@ -624,20 +643,20 @@ __global__ void __launch_bounds__(kGluThreads, 3) k_glu(const __grid_constant__ 
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
-    int64_t row = w0 < nw ? w0 / spans : p.M, span = w0 - row * spans;
-    V16 gn, un;
+    int64_t row = w0 < nw ? w0 / spans : p.M;
+    int span = (int)(w0 - row * spans);
+    int64_t in = row * p.ld + (int64_t)span * 512 + lane * 16, at = row * p.K + (int64_t)span * 512 + lane * 16;
+    V16 gn = zero16(), un = zero16();
     auto read = [&]() {
-      const int64_t col = span * 512 + lane * 16;
-      gn = un = zero16();
-      if (row < p.M && col < p.K) {
-        gn = load16(p.x, row * p.ld + col, p.wide);
-        un = load16(p.y, row * p.ld + col, p.wide);
+      if (row < p.M && (int64_t)span * 512 + lane * 16 < p.K) {
+        gn = load16(p.x, in, p.wide);
+        un = load16(p.y, in, p.wide);
       }
     };
     read();
 #pragma unroll 1
     while (row < p.M) {
-      const int64_t r = row, col = span * 512 + lane * 16;
+      const int64_t col = (int64_t)span * 512 + lane * 16, here = at;
       const bool on = col < p.K;
       const V16 gv = gn, uv = un;
       if (span != have) {
@@ -648,9 +667,13 @@ __global__ void __launch_bounds__(kGluThreads, 3) k_glu(const __grid_constant__ 
       }
       row += drow;
       span += dspan;
+      in += din;
+      at += dout;
       if (span >= spans) {
-        span -= spans;
+        span -= (int)spans;
         ++row;
+        in += cin;
+        at += cout;
       }
       read();
       f2 v[8];
@@ -659,11 +682,11 @@ __global__ void __launch_bounds__(kGluThreads, 3) k_glu(const __grid_constant__ 
       if (FMT == FMT_NVFP4 && pass == 0) {
         // values that are not finite have no share in the tensor scale
         const uint32_t ask = amax_lanes(absmax16(v), on, far, amax);
-        if (ask) amax = amax_exact<XDT, true>(p, r, col, ask, 0.0, amax);
+        if (ask) amax = amax_exact<XDT, true>(p, here, ask, 0.0, amax);
       } else {
         // 2^-21 of x' and the roundings of the scaled value
-        bad |= quant_store16<FMT, XDT, true>(p, r, col, on, v, 1.25f * 0x1p-20f, sT, isT, zero_bits16(gv) || zero_bits16(uv),
-                                               !sT_ok || far, 0.0);
+        bad |= quant_store16<FMT, XDT, true>(p, here, on, v, 1.25f * 0x1p-20f, sT, isT,
+                                             [&] { return zero_bits16(gv) || zero_bits16(uv); }, !sT_ok || far, 0.0);
       }
     }
   }
@@ -676,20 +699,22 @@ __global__ void __launch_bounds__(kGluThreads, 3) k_glu(const __grid_constant__ 
 
 // One resident wave (the NVFP4 kernels wait for the whole grid: cooperative).
 static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, bool coop, int64_t want, int threads,
-                              int sms, cudaStream_t st) {
+                              size_t smem, int sms, cudaStream_t st) {
   int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, 0);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
   if (e != cudaSuccess) return e;
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   const int64_t most = (int64_t)sms * per_sm;
   const int grid = (int)(want < most ? want : most);
   if (!coop) {
-    kern<<<grid, threads, 0, st>>>(p);
+    kern<<<grid, threads, smem, st>>>(p);
     return cudaGetLastError();
   }
   RowProblem arg = p;
   void* args[] = {&arg};
-  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(threads), args, (size_t)0, st);
+  return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(threads), args, smem, st);
 }
 
 // Few rows: a chunk a thread, for latency.  From 4 rows an SM on: CTAs of two
@@ -710,13 +735,13 @@ static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
                              : nc == 4 ? k_norm<FMT, XDT, 4>
                              : nc == 8 ? k_norm<FMT, XDT, 8>
                                        : k_norm<FMT, XDT, 0>;
-  return row_launch(kern, p, FMT == FMT_NVFP4, p.M, threads, sms, st);
+  return row_launch(kern, p, FMT == FMT_NVFP4, p.M, threads, nc > 1 ? (size_t)nc * threads * 64 : 0, sms, st);
 }
 
 template <int FMT, int XDT>
 static cudaError_t glu_launch(const RowProblem& p, int sms, cudaStream_t st) {
   const int64_t items = p.M * ((p.K + 511) / 512);
-  return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, sms, st);
+  return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, 0, sms, st);
 }
 
 // Checks shared by the two entry points.
@@ -743,7 +768,7 @@ static int row_sms(int* sms) {
   return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? DQ_OK : DQ_ECUDA;
 }
 
-static void row_fill(RowProblem* p, int64_t rows, int64_t cols, const void* col_scales, int col_dtype, int group,
+static void row_fill(RowProblem* p, int64_t rows, int64_t cols, const void* col_scales, int col_dtype,
                      const dq_outputs* out, void* workspace) {
   p->b_store = col_scales;
   p->col_dt = col_dtype;
@@ -753,7 +778,6 @@ static void row_fill(RowProblem* p, int64_t rows, int64_t cols, const void* col_
   p->K = cols;
   p->codes = static_cast<unsigned char*>(out->codes);
   p->scales = static_cast<unsigned char*>(out->block_scales);
-  p->nb = cols / group;
   p->sT_out = out->tensor_scale;
   p->hdr = static_cast<WsHeader*>(workspace);
 }
@@ -780,7 +804,7 @@ extern "C" int dq_norm_quant(const void* X, const void* residual, int x_dtype, i
   int sms = 0;
   if ((st = dq::row_sms(&sms)) != DQ_OK) return st;
   dq::RowProblem p{};
-  dq::row_fill(&p, rows, cols, col_scales, col_dtype, group, out, workspace);
+  dq::row_fill(&p, rows, cols, col_scales, col_dtype, out, workspace);
   p.x = X;
   p.y = residual;
   p.g = weight;
@@ -812,7 +836,7 @@ extern "C" int dq_glu_quant(const void* gate, const void* up, int x_dtype, int64
   int sms = 0;
   if ((st = dq::row_sms(&sms)) != DQ_OK) return st;
   dq::RowProblem p{};
-  dq::row_fill(&p, rows, cols, col_scales, col_dtype, group, out, workspace);
+  dq::row_fill(&p, rows, cols, col_scales, col_dtype, out, workspace);
   p.x = gate;
   p.y = up;
   p.ld = ld;
