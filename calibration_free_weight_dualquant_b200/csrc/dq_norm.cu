@@ -618,7 +618,7 @@ __device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const f
 }
 
 template <int FMT, int XDT>
-__global__ void __launch_bounds__(kGluThreads, 3) k_glu(const __grid_constant__ RowProblem p) {
+__global__ void __launch_bounds__(kGluThreads, 2) k_glu(const __grid_constant__ RowProblem p) {
   const int lane = threadIdx.x & 31;
   const int64_t spans = (p.K + 511) / 512;  // 512-column pieces of a row
   const int64_t w0 = (int64_t)blockIdx.x * (kGluThreads / 32) + (threadIdx.x >> 5);
