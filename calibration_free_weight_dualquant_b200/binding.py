@@ -358,39 +358,29 @@ def dq_act_quant(X: torch.Tensor, col_scales: torch.Tensor, fmt, group: Optional
     return out
 
 
-class _on:
-    """The device of the call's tensors as the current one, and ``stream`` (default: that device's current
-    stream) as the stream that new outputs and workspaces belong to."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        self.guards = []
-        if self.device.index is not None and torch.cuda.current_device() != self.device.index:
-            self.guards.append(torch.cuda.device(self.device))
-        if self.stream is not None:
-            self.guards.append(torch.cuda.stream(self.stream))
-        for g in self.guards:
-            g.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _call(device: torch.device, stream, f, *args):
+    """f(stream pointer, ...) with the device of the call's tensors as the current one, and ``stream`` (default:
+    that device's current stream) as the stream that new outputs and workspaces belong to."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return f(torch._C._cuda_getCurrentRawStream(device.index), *args)
+    with torch.cuda.device(device):
+        if stream is None:
+            return f(torch.cuda.current_stream().cuda_stream, *args)
+        with torch.cuda.stream(stream):
+            return f(stream.cuda_stream, *args)
 
 
-def _quantized(t: dict, rows: Optional[int], cols: Optional[int], f: Format, device, where: str) -> tuple:
+def _quantized(t: dict, f: Format, device, where: str) -> tuple:
     """(rows, cols) of a quantized matrix {"codes", "block_scales", "tensor_scale"}; DQError unless its tensors
     are the format's, on `device`."""
     codes, scales = t["codes"], t["block_scales"]
     if codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.device != device:
         raise DQError(1, where + ": codes must be a contiguous 2-D uint8 tensor on the call's device")
-    r, c = codes.shape[0], codes.shape[1] * (1 if f == Format.MXFP8 else 2)
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise DQError(1, where + ": codes [%d][%d columns] do not fit the call" % (r, c))
+    r, c = codes.shape
+    if f != Format.MXFP8:
+        c *= 2
     if (scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.device != device
-            or tuple(scales.shape) != (r, c // DEFAULT_GROUP[f])):
+            or scales.shape != (r, c // DEFAULT_GROUP[f])):
         raise DQError(1, where + ": block_scales must be contiguous uint8 [rows][cols/group] on the call's device")
     if f == Format.NVFP4:
         s = t.get("tensor_scale")
@@ -400,30 +390,30 @@ def _quantized(t: dict, rows: Optional[int], cols: Optional[int], f: Format, dev
 
 
 def _quantized_struct(t: dict, f: Format) -> _Outputs:
-    s = t.get("tensor_scale")
     return _Outputs(t["codes"].data_ptr(), t["block_scales"].data_ptr(),
-                    s.data_ptr() if f == Format.NVFP4 or s is not None else None, None, None)
+                    t["tensor_scale"].data_ptr() if f == Format.NVFP4 else None, None, None)
+
+
+_PRODUCT_FORMATS = {k: f for f in (Format.NVFP4, Format.MXFP4, Format.MXFP8) for k in (f, int(f), f.name.lower())}
 
 
 def _product_format(fmt, group: Optional[int], where: str) -> Format:
-    f = _fmt(fmt)
-    if f not in (Format.NVFP4, Format.MXFP4, Format.MXFP8):
+    f = _PRODUCT_FORMATS.get(fmt)
+    if f is None:
+        _fmt(fmt)  # an unknown name is an error of its own
         raise DQError(2, where + ": nvfp4, mxfp4 and mxfp8 only")
     if group is not None and group != DEFAULT_GROUP[f]:
         raise DQError(2, where + ": group %d" % DEFAULT_GROUP[f])
     return f
 
 
-def _workspace_for(workspace: Optional[torch.Tensor], nbytes: int, device, where: str) -> torch.Tensor:
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _check_workspace(workspace: torch.Tensor, device, where: str):
     if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise DQError(1, where + ": workspace must be a contiguous uint8 tensor on the call's device")
-    return workspace
 
 
-def _raise_device_status(lib, workspace: torch.Tensor, stream_ptr: int, where: str):
-    st = lib.dq_sync_status(workspace.data_ptr(), stream_ptr)
+def _raise_device_status(workspace: torch.Tensor, stream_ptr: int, where: str):
+    st = _lib.dq_sync_status(workspace.data_ptr(), stream_ptr)
     if st != 0:
         raise DQError(st, where + " (device)")
 
@@ -438,47 +428,57 @@ def dq_matmul(X: dict, W: dict, fmt, group: Optional[int] = None, out: Optional[
 
     X and W are dicts with "codes", "block_scales" and (NVFP4) "tensor_scale", as dq_act_quant, dq_norm_quant,
     dq_glu_quant and dq_solve return them, both in ``fmt`` (nvfp4, mxfp4 or mxfp8).  ``out`` (its dtype then
-    counts, not ``out_dtype``) and ``workspace`` keep the call free of allocations; ``check`` waits for the
-    stream and raises on a device-reported status."""
-    lib = load_library()
+    counts, not ``out_dtype``) keeps the call free of allocations; ``check`` waits for the stream and raises on
+    a device-reported status, which a ``workspace`` of MATMUL_WORKSPACE_BYTES reports later without it."""
+    load_library()
     f = _product_format(fmt, group, "dq_matmul")
-    if not X["codes"].is_cuda:
+    codes = X["codes"]
+    if not codes.is_cuda:
         raise DQError(1, "dq_matmul: X must be on a CUDA device")
-    dev = X["codes"].device
-    tokens, cols = _quantized(X, None, None, f, dev, "dq_matmul: X")
-    rows, _ = _quantized(W, None, cols, f, dev, "dq_matmul: W")
-    with _on(dev, stream) as sp:
-        if out is None:
-            if out_dtype not in _DTYPES:
-                raise DQError(1, "dq_matmul: out_dtype must be float32, bfloat16 or float16")
-            out = torch.empty((tokens, rows), dtype=out_dtype, device=dev)
-        elif out.dtype not in _DTYPES or tuple(out.shape) != (tokens, rows) or not out.is_contiguous() or out.device != dev:
-            raise DQError(1, "dq_matmul: out must be contiguous f32/bf16/f16 [tokens, rows] on the call's device")
-        workspace = _workspace_for(workspace, MATMUL_WORKSPACE_BYTES, dev, "dq_matmul")
-        xo, wo = _quantized_struct(X, f), _quantized_struct(W, f)
-        st = lib.dq_matmul(ctypes.byref(xo), tokens, ctypes.byref(wo), rows, cols, int(f), DEFAULT_GROUP[f],
-                           out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(), workspace.numel(), sp)
-        if st != 0:
-            raise DQError(st, "dq_matmul")
-        if check:
-            _raise_device_status(lib, workspace, sp, "dq_matmul")
-    return out
+    return _call(codes.device, stream, _matmul, codes, X, W, f, out, out_dtype, workspace, check)
 
 
-def _row_outputs(out: Optional[dict], rows: int, cols: int, f: Format, device, where: str) -> dict:
+def _matmul(sp, codes, X, W, f, out, out_dtype, workspace, check):
+    dev = codes.device
+    tokens, cols = _quantized(X, f, dev, "dq_matmul: X")
+    rows, wcols = _quantized(W, f, dev, "dq_matmul: W")
+    if wcols != cols:
+        raise DQError(1, "dq_matmul: W has %d columns and X %d" % (wcols, cols))
     if out is None:
-        g = DEFAULT_GROUP[f]
-        return {"codes": torch.empty((rows, code_cols(cols, f)), dtype=torch.uint8, device=device),
-                "block_scales": torch.empty((rows, cols // g), dtype=torch.uint8, device=device),
-                "tensor_scale": torch.empty(1, dtype=torch.float32, device=device)}
-    _quantized(out, rows, cols, f, device, where)
+        if out_dtype not in _DTYPES:
+            raise DQError(1, "dq_matmul: out_dtype must be float32, bfloat16 or float16")
+        out = codes.new_empty((tokens, rows), dtype=out_dtype)
+    elif out.dtype not in _DTYPES or out.shape != (tokens, rows) or not out.is_contiguous() or out.device != dev:
+        raise DQError(1, "dq_matmul: out must be contiguous f32/bf16/f16 [tokens, rows] on the call's device")
+    if workspace is not None:
+        _check_workspace(workspace, dev, "dq_matmul")
+    elif check:
+        workspace = codes.new_empty(MATMUL_WORKSPACE_BYTES)
+    st = _lib.dq_matmul(_quantized_struct(X, f), tokens, _quantized_struct(W, f), rows, cols, f, DEFAULT_GROUP[f],
+                        out.data_ptr(), _DTYPES[out.dtype], None if workspace is None else workspace.data_ptr(),
+                        0 if workspace is None else workspace.numel(), sp)
+    if st != 0:
+        raise DQError(st, "dq_matmul")
+    if check:
+        _raise_device_status(workspace, sp, "dq_matmul")
     return out
 
 
-def _channel_vector(t: Optional[torch.Tensor], cols: int, dtypes, device, where: str):
-    if t is not None and (t.dtype not in dtypes or t.numel() != cols or not t.is_contiguous() or t.device != device):
+def _row_outputs(out: Optional[dict], like: torch.Tensor, rows: int, cols: int, f: Format, where: str) -> dict:
+    if out is None:
+        out = {"codes": like.new_empty((rows, cols if f == Format.MXFP8 else cols // 2), dtype=torch.uint8),
+               "block_scales": like.new_empty((rows, cols // DEFAULT_GROUP[f]), dtype=torch.uint8)}
+        if f == Format.NVFP4:
+            out["tensor_scale"] = like.new_empty(1, dtype=torch.float32)
+    elif _quantized(out, f, like.device, where) != (rows, cols):
+        raise DQError(1, where + " must be [%d][%d columns]" % (rows, cols))
+    return out
+
+
+def _channel_vector(t: torch.Tensor, cols: int, dtypes, device, where: str) -> int:
+    if t.dtype not in dtypes or t.numel() != cols or not t.is_contiguous() or t.device != device:
         raise DQError(1, where + " must be a contiguous 16-bit float [cols] tensor on the call's device")
-    return None if t is None else t.data_ptr()
+    return t.data_ptr()
 
 
 _HALVES = (torch.bfloat16, torch.float16)
@@ -492,37 +492,40 @@ def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: O
     scales, quantized row-wise in ``fmt`` (mxfp8, mxfp4 or nvfp4).  Returns the quantized matrix with
     out["residual"] = h (with a residual; ``residual_out`` may be X or the residual itself).  A non-finite row
     gets NaN scales; ``check`` waits and raises on it."""
-    lib = load_library()
+    load_library()
     f = _product_format(fmt, group, "dq_norm_quant")
     if not X.is_cuda or X.dtype not in _HALVES or not X.is_contiguous() or X.dim() != 2:
         raise DQError(1, "dq_norm_quant: X must be a contiguous 2-D bf16/f16 CUDA tensor")
-    rows, cols = X.shape
-    dev = X.device
     for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-        if t is not None and (t.dtype != X.dtype or t.shape != X.shape or not t.is_contiguous() or t.device != dev):
+        if t is not None and (t.dtype != X.dtype or t.shape != X.shape or not t.is_contiguous() or t.device != X.device):
             raise DQError(1, "dq_norm_quant: %s must match X" % name)
     if residual is None and residual_out is not None:
         raise DQError(1, "dq_norm_quant: residual_out without a residual")
-    gp = _channel_vector(weight, cols, (X.dtype,), dev, "dq_norm_quant: weight (in X's dtype)")
-    bp = _channel_vector(col_scales, cols, _HALVES, dev, "dq_norm_quant: col_scales")
-    with _on(dev, stream) as sp:
-        nbytes = lib.dq_norm_workspace_bytes(rows, cols, int(f), DEFAULT_GROUP[f])
-        if nbytes == 0:
-            raise DQError(1, "dq_norm_workspace_bytes")
-        out = _row_outputs(out, rows, cols, f, dev, "dq_norm_quant: out")
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(X)
-        workspace = _workspace_for(workspace, nbytes, dev, "dq_norm_quant")
-        o = _quantized_struct(out, f)
-        st = lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), _DTYPES[X.dtype], rows,
-                               cols, gp, eps, bp, 1 if col_scales is None else _DTYPES[col_scales.dtype], int(f),
-                               DEFAULT_GROUP[f], ctypes.byref(o),
-                               None if residual_out is None else residual_out.data_ptr(), workspace.data_ptr(),
-                               workspace.numel(), sp)
-        if st != 0:
-            raise DQError(st, "dq_norm_quant")
-        if check:
-            _raise_device_status(lib, workspace, sp, "dq_norm_quant")
+    return _call(X.device, stream, _norm_quant, X, weight, col_scales, f, residual, eps, out, residual_out, workspace,
+                 check)
+
+
+def _norm_quant(sp, X, weight, col_scales, f, residual, eps, out, residual_out, workspace, check):
+    rows, cols = X.shape
+    dev = X.device
+    gp = None if weight is None else _channel_vector(weight, cols, (X.dtype,), dev,
+                                                     "dq_norm_quant: weight (in X's dtype)")
+    bp = None if col_scales is None else _channel_vector(col_scales, cols, _HALVES, dev, "dq_norm_quant: col_scales")
+    out = _row_outputs(out, X, rows, cols, f, "dq_norm_quant: out")
+    if residual is not None and residual_out is None:
+        residual_out = X.new_empty((rows, cols))
+    if workspace is None:
+        workspace = X.new_empty(ACT_WORKSPACE_BYTES + (8 * rows if f == Format.NVFP4 else 0), dtype=torch.uint8)
+    else:
+        _check_workspace(workspace, dev, "dq_norm_quant")
+    st = _lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), _DTYPES[X.dtype], rows, cols,
+                            gp, eps, bp, 1 if col_scales is None else _DTYPES[col_scales.dtype], f, DEFAULT_GROUP[f],
+                            _quantized_struct(out, f), None if residual is None else residual_out.data_ptr(),
+                            workspace.data_ptr(), workspace.numel(), sp)
+    if st != 0:
+        raise DQError(st, "dq_norm_quant")
+    if check:
+        _raise_device_status(workspace, sp, "dq_norm_quant")
     if residual is not None:
         out["residual"] = residual_out
     out["workspace"] = workspace
@@ -534,35 +537,42 @@ def dq_glu_quant(X, col_scales: Optional[torch.Tensor], fmt, group: Optional[int
     """Enqueue dq_glu_quant: silu(gate) * up times the column inverse scales, quantized row-wise in ``fmt``
     (mxfp8, mxfp4 or nvfp4).  X is one tensor [tokens, 2 cols], gate left of up (a product over stacked gate and
     up weights), or a pair (gate, up) of [tokens, cols] tensors with one row stride."""
-    lib = load_library()
+    load_library()
     f = _product_format(fmt, group, "dq_glu_quant")
-    if isinstance(X, torch.Tensor):
-        if X.dim() != 2 or X.shape[1] % 2 != 0:
-            raise DQError(1, "dq_glu_quant: X must be 2-D with an even number of columns")
-        gate, up = X[:, :X.shape[1] // 2], X[:, X.shape[1] // 2:]
-    else:
-        gate, up = X
-    for t in (gate, up):
+    one = isinstance(X, torch.Tensor)
+    gate, up = (X, X) if one else X
+    for t in (gate,) if one else (gate, up):
         if not t.is_cuda or t.dtype not in _HALVES or t.dim() != 2 or t.stride(1) != 1:
             raise DQError(1, "dq_glu_quant: gate and up must be 2-D bf16/f16 CUDA tensors with adjacent columns")
-    if gate.shape != up.shape or gate.dtype != up.dtype or gate.device != up.device or (
-            gate.shape[0] > 1 and gate.stride(0) != up.stride(0)):
+    if one and X.shape[1] % 2 != 0:
+        raise DQError(1, "dq_glu_quant: X must have an even number of columns")
+    if not one and (gate.shape != up.shape or gate.dtype != up.dtype or gate.device != up.device
+                    or (gate.shape[0] > 1 and gate.stride(0) != up.stride(0))):
         raise DQError(1, "dq_glu_quant: gate and up must agree in shape, dtype, device and row stride")
+    return _call(gate.device, stream, _glu_quant, gate, up, one, col_scales, f, out, workspace, check)
+
+
+def _glu_quant(sp, gate, up, one, col_scales, f, out, workspace, check):
     rows, cols = gate.shape
-    ld = gate.stride(0) if rows > 1 else cols
-    dev = gate.device
-    bp = _channel_vector(col_scales, cols, _HALVES, dev, "dq_glu_quant: col_scales")
-    with _on(dev, stream) as sp:
-        out = _row_outputs(out, rows, cols, f, dev, "dq_glu_quant: out")
-        workspace = _workspace_for(workspace, ACT_WORKSPACE_BYTES, dev, "dq_glu_quant")
-        o = _quantized_struct(out, f)
-        st = lib.dq_glu_quant(gate.data_ptr(), up.data_ptr(), _DTYPES[gate.dtype], rows, cols, ld, bp,
-                              1 if col_scales is None else _DTYPES[col_scales.dtype], int(f), DEFAULT_GROUP[f],
-                              ctypes.byref(o), workspace.data_ptr(), workspace.numel(), sp)
-        if st != 0:
-            raise DQError(st, "dq_glu_quant")
-        if check:
-            _raise_device_status(lib, workspace, sp, "dq_glu_quant")
+    gp, upp = gate.data_ptr(), up.data_ptr()
+    if one:
+        cols //= 2
+        upp += 2 * cols
+    ld = gate.stride(0) if rows > 1 else cols + (-cols % 8)
+    bp = None if col_scales is None else _channel_vector(col_scales, cols, _HALVES, gate.device,
+                                                         "dq_glu_quant: col_scales")
+    out = _row_outputs(out, gate, rows, cols, f, "dq_glu_quant: out")
+    if workspace is None:
+        workspace = gate.new_empty(ACT_WORKSPACE_BYTES, dtype=torch.uint8)
+    else:
+        _check_workspace(workspace, gate.device, "dq_glu_quant")
+    st = _lib.dq_glu_quant(gp, upp, _DTYPES[gate.dtype], rows, cols, ld, bp,
+                           1 if col_scales is None else _DTYPES[col_scales.dtype], f, DEFAULT_GROUP[f],
+                           _quantized_struct(out, f), workspace.data_ptr(), workspace.numel(), sp)
+    if st != 0:
+        raise DQError(st, "dq_glu_quant")
+    if check:
+        _raise_device_status(workspace, sp, "dq_glu_quant")
     out["workspace"] = workspace
     return out
 

@@ -30,7 +30,7 @@ struct MatmulProblem {
   void* y;
   int y_dt;
   int64_t T, N, K;
-  WsHeader* hdr;
+  unsigned* flags;  // the workspace's status word, or NULL
 };
 
 // The tensor scales' product as f1 * f2, applied one after the other: f2 is 1
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256) k_matmul_any(MatmulProblem p) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int64_t tiles_n = (p.N + 63) / 64, nb = p.K / G;
   const int64_t t0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * 64;
-  if (blockIdx.x == 0 && tid == 0) p.hdr->flags = 0;
+  if (blockIdx.x == 0 && tid == 0 && p.flags) *p.flags = 0;
   float acc[4][4] = {};
   for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
 #pragma unroll
@@ -228,7 +228,7 @@ __device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned
   const unsigned long long t0 = global_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (global_ns() - t0 > kWaitLimitNs) {
-      atomicOr(flags, kFlagTimeout);
+      if (flags) atomicOr(flags, kFlagTimeout);
       return false;
     }
   }
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   const int64_t nk = (p.K + F::kTileK - 1) / F::kTileK;
   const int64_t k0 = nk * rank / l.split;
   const int n = (int)(nk * (rank + 1) / l.split - k0);  // at least 1: split <= nk
-  unsigned* flags = &p.hdr->flags;
+  unsigned* flags = p.flags;
   if (threadIdx.x == 0) {
     for (int i = 0; i < l.stages; ++i) {
       mbar_init(&full_t[i], 1);
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     }
     mbar_init(&acc_full, 1);
     mbar_fence_init();
-    if (blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
+    if (blockIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   }
   if (warp == 1) tc_alloc<1, G::kAlloc>(smem_u32(&tmem_base));
   tc_fence_before();
@@ -415,10 +415,15 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     const int64_t nn = n0 + 32 * q + lane;
     float* part = reinterpret_cast<float*>(ring);  // [token][128 features]: the ring is idle now
 #pragma unroll 1
-    for (int c = 0; c < tv && ok; c += 16) {
+    for (int c = 0; c < tv; c += 16) {
       uint32_t v[16];
-      tc_load16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
-      tc_load_wait16(v);
+      if (ok) {
+        tc_load16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+        tc_load_wait16(v);
+      } else {  // a wait ran out: no number that looks like a result
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0x7FC00000u;
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         if (c + i < tv) {
@@ -543,9 +548,23 @@ __device__ __forceinline__ void store_turned(const MatmulProblem& p, float* turn
     }
 }
 
+// A wait ran out: this warp's part of the tiles i, i + pairs, ... becomes NaN, so
+// that nothing looks like a result.
+template <bool OUT32>
+static __device__ __noinline__ void pair_give_up(const MatmulProblem& p, const PairLaunch& l, unsigned i, unsigned pairs,
+                                                 int rank, int warp) {
+  for (; i < l.tiles; i += pairs) {
+    int64_t m, n;
+    pair_tile(l, i, m, n);
+    const int64_t t = m * 256 + rank * 128 + 32 * (warp & 3) + (threadIdx.x & 31), n0 = n * 256 + 128 * (warp >> 2);
+    if (t < p.T)
+      for (int64_t c = n0; c < p.N && c < n0 + 128; ++c) y_store(p.y, p.y_dt, t * p.N + c, __uint_as_float(0x7FC00000u));
+  }
+}
+
 template <int FMT, bool OUT32>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    k_matmul_pair(MatmulProblem p, PairLaunch l, const __grid_constant__ CUtensorMap wmap,
+    k_matmul_pair(const __grid_constant__ MatmulProblem p, const __grid_constant__ PairLaunch l, const __grid_constant__ CUtensorMap wmap,
                   const __grid_constant__ CUtensorMap xmap) {
   using G = PairGeo<FMT>;
   using F = TcFormat<FMT>;
@@ -559,7 +578,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const unsigned pair = blockIdx.x / 2, pairs = gridDim.x / 2;
   const int nk = (int)((p.K + F::kTileK - 1) / F::kTileK);
   const int64_t nb = p.K / F::kGroup;
-  unsigned* flags = &p.hdr->flags;
+  unsigned* flags = p.flags;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       mbar_init(&full_t[i], 1);
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     mbar_init(&acc_full, 1);
     mbar_init(&acc_empty, 2 * kPairEpilogue);
     mbar_fence_init();
-    if (blockIdx.x == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
+    if (blockIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   }
   if (warp == 9) tc_alloc<2, 512>(smem_u32(&tmem_base));
   tc_fence_before();
@@ -658,7 +677,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (unsigned i = pair; i < l.tiles; i += pairs, turn ^= 1) {
       int64_t m, n;
       pair_tile(l, i, m, n);
-      if (!__all_sync(0xffffffffu, mm_wait(&acc_full, turn, flags))) break;
+      if (!__all_sync(0xffffffffu, mm_wait(&acc_full, turn, flags))) {
+        pair_give_up<OUT32>(p, l, i, pairs, rank, warp);
+        break;
+      }
       tc_fence_after();
       const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
       const int64_t t0 = m * 256 + rank * 128 + 32 * q, t = t0 + lane, nn = n * 256 + 128 * half;
@@ -868,8 +890,8 @@ extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* 
                              (uintptr_t)W->tensor_scale % 4 != 0))
     return DQ_EINVAL;
   if ((uintptr_t)Y % (y_dtype == DQ_F32 ? 4 : 2) != 0) return DQ_EINVAL;
-  if (!workspace || (uintptr_t)workspace % 256 != 0) return DQ_EINVAL;
-  if (workspace_bytes < DQ_MATMUL_WORKSPACE_BYTES) return DQ_EWORKSPACE;
+  if ((uintptr_t)workspace % 256 != 0) return DQ_EINVAL;
+  if (workspace && workspace_bytes < DQ_MATMUL_WORKSPACE_BYTES) return DQ_EWORKSPACE;
   dq::MatmulProblem p{};
   p.xq = static_cast<const unsigned char*>(X->codes);
   p.xs = static_cast<const unsigned char*>(X->block_scales);
@@ -884,7 +906,7 @@ extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* 
   p.T = tokens;
   p.N = rows;
   p.K = cols;
-  p.hdr = static_cast<dq::WsHeader*>(workspace);
+  p.flags = workspace ? &static_cast<dq::WsHeader*>(workspace)->flags : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ECUDA;

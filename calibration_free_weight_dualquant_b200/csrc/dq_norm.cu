@@ -340,6 +340,18 @@ __device__ __forceinline__ void row_grid_barrier(WsHeader* hdr) {
   __syncthreads();
 }
 
+// A grid of one CTA clears its own header.
+__device__ __forceinline__ void row_clear_header(WsHeader* hdr) {
+  if (gridDim.x == 1) {
+    if (threadIdx.x == 0) {
+      hdr->flags = 0;
+      hdr->gbar = 0;
+      hdr->amax_scaled = 0;
+    }
+    __syncthreads();
+  }
+}
+
 // Tensor scale from the bits of max |x'| (fp64) over the call.
 __device__ __forceinline__ float tensor_scale(unsigned long long bits) {
   const double amax = __longlong_as_double((long long)bits);
@@ -437,6 +449,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
   const int chunks = (int)(p.K / 16);
   const int trips = NC > 0 ? 1 : (chunks + nt - 1) / nt;
   const void* hsrc = p.y ? p.h : p.x;
+  row_clear_header(p.hdr);
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
@@ -628,6 +641,7 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu(const __grid_constant__ 
   // ... and as elements of the inputs and outputs, without and with a carry into the next row
   const int64_t din = drow * p.ld + dspan * 512, dout = drow * p.K + dspan * 512;
   const int64_t cin = p.ld - spans * 512, cout = p.K - spans * 512;
+  row_clear_header(p.hdr);
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
@@ -698,17 +712,25 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu(const __grid_constant__ 
 // Host side.
 
 // One resident wave (the NVFP4 kernels wait for the whole grid: cooperative).
+// A single CTA clears the header itself; more of them need it cleared before.
+// Up to one CTA an SM is resident whatever the kernel's registers, so the
+// occupancy is asked for beyond that only (a microsecond of the host's time).
 static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, bool coop, int64_t want, int threads,
                               size_t smem, int sms, cudaStream_t st) {
-  int per_sm = 0;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem);
-  if (e != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t most = (int64_t)sms * per_sm;
-  const int grid = (int)(want < most ? want : most);
-  if (!coop) {
+  cudaError_t e;
+  if (smem > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+    return e;
+  int grid = (int)(want < sms ? want : sms);
+  if (want > sms) {
+    int per_sm = 0;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    const int64_t most = (int64_t)sms * per_sm;
+    grid = (int)(want < most ? want : most);
+  }
+  if (grid > 1 && (e = cudaMemsetAsync(p.hdr, 0, sizeof(WsHeader), st)) != cudaSuccess) return e;
+  if (!coop || grid == 1) {
     kern<<<grid, threads, smem, st>>>(p);
     return cudaGetLastError();
   }
@@ -814,7 +836,6 @@ extern "C" int dq_norm_quant(const void* X, const void* residual, int x_dtype, i
   p.wide = ((uintptr_t)X | (uintptr_t)residual | (uintptr_t)residual_out) % 32 == 0;  // a row is a multiple of 32 bytes
   p.rstd = reinterpret_cast<double*>(static_cast<unsigned char*>(workspace) + DQ_ACT_WORKSPACE_BYTES);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(dq::WsHeader), s) != cudaSuccess) return DQ_ECUDA;
   cudaError_t e;
   if (format == DQ_NVFP4)
     e = x_dtype == DQ_BF16 ? dq::norm_launch<dq::FMT_NVFP4, dq::DT_BF16>(p, sms, s) : dq::norm_launch<dq::FMT_NVFP4, dq::DT_F16>(p, sms, s);
@@ -842,7 +863,6 @@ extern "C" int dq_glu_quant(const void* gate, const void* up, int x_dtype, int64
   p.ld = ld;
   p.wide = ((uintptr_t)gate | (uintptr_t)up | (uintptr_t)(2 * ld)) % 32 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(dq::WsHeader), s) != cudaSuccess) return DQ_ECUDA;
   cudaError_t e;
   if (format == DQ_NVFP4)
     e = x_dtype == DQ_BF16 ? dq::glu_launch<dq::FMT_NVFP4, dq::DT_BF16>(p, sms, s) : dq::glu_launch<dq::FMT_NVFP4, dq::DT_F16>(p, sms, s);

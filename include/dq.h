@@ -322,7 +322,8 @@ int dq_act_quant(const void* X, int x_dtype, int64_t rows, int64_t cols, const v
  * others take a slower kernel.
  * The workspace (DQ_MATMUL_WORKSPACE_BYTES, 256-byte aligned) reports a bounded
  * wait that ran out through dq_sync_status (DQ_ECUDA).  Calls that may run at
- * the same time need a workspace each. */
+ * the same time need a workspace each.  It may be NULL: then such a wait shows
+ * in the outputs alone, which it makes NaN either way. */
 int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format, int group,
               void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 

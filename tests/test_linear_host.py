@@ -33,7 +33,7 @@ def matmul(lib, tokens=4, rows=8, cols=64, fmt=3, group=32, y=FAKE, dt=1, ws=FAK
     (dict(tokens=0), 1), (dict(rows=0), 1), (dict(cols=0), 1), (dict(tokens=-1), 1), (dict(cols=48), 1),
     (dict(fmt=-1), 1), (dict(fmt=6), 1), (dict(fmt=0, group=64), 2), (dict(fmt=1), 2), (dict(fmt=4), 2),
     (dict(fmt=2, group=32), 2), (dict(fmt=3, group=16), 2), (dict(dt=3), 1), (dict(y=None), 1), (dict(y=FAKE + 1), 1),
-    (dict(dt=0, y=FAKE + 2), 1), (dict(ws=None), 1), (dict(ws=FAKE + 16), 1), (dict(nbytes=255), 3),
+    (dict(dt=0, y=FAKE + 2), 1), (dict(ws=FAKE + 16), 1), (dict(nbytes=255), 3),
     (dict(X=outs(codes=None)), 1), (dict(W=outs(scales=None)), 1), (dict(fmt=2, group=16, X=outs(sT=None)), 1),
     (dict(fmt=2, group=16, W=outs(sT=FAKE + 2)), 1), (dict(tokens=2 ** 31), 2), (dict(tokens=2 ** 30, rows=2 ** 30), 2),
 ])
