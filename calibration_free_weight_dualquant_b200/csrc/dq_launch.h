@@ -1,0 +1,34 @@
+// dq_launch.h -- launch of the linear layer's kernels, optionally in clusters,
+// with programmatic stream serialization: a kernel may be set up (barriers,
+// tensor memory, its grid's launch) while the one before it in the stream
+// finishes.  Every thread of such a kernel calls griddep_wait() before it
+// touches global memory.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+namespace dq {
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_early(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, int cluster,
+                                cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace dq

@@ -7,7 +7,6 @@
 // the column scales b are in q_x already).  Sums are held in fp32 and rounded
 // once, after the tensor scales, to the output type.
 #include <climits>
-#include <cstring>
 
 #include <cuda.h>
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
@@ -16,6 +15,7 @@
 #include "dq_device.cuh"
 #include "dq_fast.cuh"
 #include "dq_internal.h"
+#include "dq_launch.h"
 #include "dq_tc.cuh"
 
 namespace dq {
@@ -58,6 +58,32 @@ __device__ __forceinline__ void y_store(void* y, int dt, int64_t i, float v) {
     reinterpret_cast<__half*>(y)[i] = __float2half_rn(v);
 }
 
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dt) {
+  uint32_t r;
+  if (dt == DT_BF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four neighbouring outputs from element i, `n` of them inside the row.  vec:
+// such fours start at multiples of their size.
+__device__ __forceinline__ void y_store4(void* y, int dt, int64_t i, const float* v, int64_t n, bool vec) {
+  if (vec && n >= 4) {
+    if (dt == DT_F32) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(y) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      const uint32_t a = pack16(v[0], v[1], dt), b = pack16(v[2], v[3], dt);
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(y) + i) = make_uint2(a, b);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) y_store(y, dt, i + k, v[k]);
+  }
+}
+
 // Grid value of one code.
 template <int FMT>
 __device__ __forceinline__ float code_value(const unsigned char* q, int64_t at) {
@@ -87,6 +113,8 @@ __global__ void __launch_bounds__(256) k_matmul_any(MatmulProblem p) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int64_t tiles_n = (p.N + 63) / 64, nb = p.K / G;
   const int64_t t0 = blockIdx.x / tiles_n * 64, n0 = blockIdx.x % tiles_n * 64;
+  griddep_wait();
+  griddep_launch_dependents();
   if (blockIdx.x == 0 && tid == 0 && p.flags) *p.flags = 0;
   float acc[4][4] = {};
   for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
@@ -141,8 +169,7 @@ __global__ void __launch_bounds__(256) k_matmul_any(MatmulProblem p) {
 template <int FMT>
 static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
   const int64_t tiles = (p.T + 63) / 64 * ((p.N + 63) / 64);
-  k_matmul_any<FMT><<<(unsigned)tiles, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(k_matmul_any<FMT>, (unsigned)tiles, 256, 0, 1, st, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -177,9 +204,11 @@ struct MmGeo {
 };
 
 // Block scales of a lane's four rows (row0 + lane + 32 q): the 32-byte piece
-// `piece` of each row, one memory sector, as words w[q][0 .. 7]; zeros past the
-// matrix.  U: bytes a load, a divisor of the row's bytes and of its address,
-// so no load straddles the row's end.
+// `piece` of each row, one memory sector where rows are aligned, as words
+// w[q][0 .. 7]; zeros past the matrix.  U: what the address and the length of
+// every row are multiples of, 32, 16 or (1) nothing.  With 1, three aligned
+// 16-byte reads are shifted into place; pieces whose aligned window leaves the
+// scales' memory are read by bytes.
 template <int U>
 __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t piece,
                                             uint32_t (*w)[8]) {
@@ -190,35 +219,48 @@ __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0
     const int64_t left = r < rows ? nb - piece * 32 : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[q][j] = 0;
+    if constexpr (U == 32) {
+      if (left > 0)
+        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3]), "=r"(w[q][4]), "=r"(w[q][5]), "=r"(w[q][6]),
+              "=r"(w[q][7])
+            : "l"(p));
+    } else if constexpr (U == 16) {
 #pragma unroll
-    for (int i = 0; i < 32 / U; ++i) {
-      if (i * U < left) {
-        if constexpr (U == 32) {
-          asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-              : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3]), "=r"(w[q][4]), "=r"(w[q][5]), "=r"(w[q][6]),
-                "=r"(w[q][7])
-              : "l"(p));
-        } else if constexpr (U == 16) {
+      for (int i = 0; i < 2; ++i)
+        if (16 * i < left) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
           w[q][4 * i] = v.x, w[q][4 * i + 1] = v.y, w[q][4 * i + 2] = v.z, w[q][4 * i + 3] = v.w;
-        } else if constexpr (U == 4) {
-          w[q][i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-        } else if constexpr (U == 2) {
-          w[q][i / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) << (16 * (i & 1));
-        } else {
-          w[q][i / 4] |= (uint32_t)__ldg(p + i) << (8 * (i & 3));
+        }
+    } else if (left > 0) {
+      const unsigned sh = (unsigned)(uintptr_t)p & 15u;
+      const unsigned char* a = p - sh;
+      if (a >= s && a + 48 <= s + rows * nb) {
+        const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(a)), v1 = __ldg(reinterpret_cast<const uint4*>(a) + 1),
+                    v2 = __ldg(reinterpret_cast<const uint4*>(a) + 2);
+        uint32_t t[12] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w, v2.x, v2.y, v2.z, v2.w};
+#pragma unroll
+        for (int j = 0; j < 10; ++j) t[j] = sh & 8u ? t[j + 2] : t[j];
+#pragma unroll
+        for (int j = 0; j < 9; ++j) t[j] = sh & 4u ? t[j + 1] : t[j];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t have = left - 4 * j;  // bytes of this word that belong to the row
+          const uint32_t v = __funnelshift_r(t[j], t[j + 1], 8 * (sh & 3u));
+          w[q][j] = have >= 4 ? v : (have > 0 ? v & (0xFFFFFFFFu >> (32 - 8 * (int)have)) : 0u);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint32_t v = 0;
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i)
+            if (4 * j + i < left) v |= (uint32_t)p[4 * j + i] << (8 * i);
+          w[q][j] = v;
         }
       }
     }
   }
-}
-
-// The same out of line for scales at odd addresses (1- and 2-byte loads, up to
-// 128 a lane): inlined, they took the registers of the paths that matter.
-template <int U>
-static __device__ __noinline__ void load_scales_far(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb,
-                                                    int64_t piece, uint32_t (*w)[8]) {
-  load_scales<U>(s, row0, rows, nb, piece, w);
 }
 
 // Bounded wait for a ring barrier, by the clock alone: the header's flags may
@@ -258,21 +300,18 @@ struct ScaleTurn {
 // A warp's share of one block's scales of the K tiles k0 .. k0 + n - 1.  Slot t
 // of the ring starts at ring + t * slot_bytes; the words of K tile u of a piece
 // and scale word j are the 512-byte block u * kAtoms + j, block_bytes apart.
-// PAIR: the arrival goes to the pair's even CTA.
+// PAIR: the arrival goes to the cluster's CTA `leader`.
 template <bool PAIR, int U>
 __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0, int64_t rows,
                                            int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes, int block_bytes,
-                                           uint64_t* full, uint64_t* empty, unsigned* flags) {
+                                           uint64_t* full, uint64_t* empty, unsigned* flags, uint32_t leader) {
   const int lane = threadIdx.x & 31;
   const int last = (k0 + n - 1) / tiles_per_piece;
 #pragma unroll 1
   for (int piece = k0 / tiles_per_piece; piece <= last; ++piece, ++t.piece) {
     if ((int)(t.piece & 1) != t.turn) continue;
     uint32_t w[4][8];
-    if constexpr (U >= 4)
-      load_scales<U>(s, row0, rows, nb, piece, w);
-    else
-      load_scales_far<U>(s, row0, rows, nb, piece, w);
+    load_scales<U>(s, row0, rows, nb, piece, w);
     if (!__all_sync(0xffffffffu, mm_wait(&empty[t.turn], ((t.piece >> 1) & 1) ^ 1, flags))) return false;
     unsigned char* dst = ring + t.turn * slot_bytes + lane * 16;
 #pragma unroll
@@ -282,7 +321,7 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
     __syncwarp();
     if (lane == 0) {
       if (PAIR)
-        mbar_arrive_cluster(&full[t.turn], 0);
+        mbar_arrive_cluster(&full[t.turn], leader);
       else
         mbar_arrive(&full[t.turn]);
     }
@@ -290,28 +329,24 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
   return true;
 }
 // `unit`: the largest power of two (32 at most) that divides the scales' address
-// and the row.
+// and the row's length.
 template <bool PAIR>
 __device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0,
                                            int64_t rows, int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes,
-                                           int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags) {
+                                           int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags, uint32_t leader) {
 #define DQ_SCALE_LOOP(U) \
-  scale_loop<PAIR, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, flags)
-  switch (unit) {
-    case 32: return DQ_SCALE_LOOP(32);
-    case 16: return DQ_SCALE_LOOP(16);
-    case 8:
-    case 4: return DQ_SCALE_LOOP(4);
-    case 2: return DQ_SCALE_LOOP(2);
-    default: return DQ_SCALE_LOOP(1);
-  }
+  scale_loop<PAIR, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, flags, leader)
+  if (unit == 32) return DQ_SCALE_LOOP(32);
+  if (unit == 16) return DQ_SCALE_LOOP(16);
+  return DQ_SCALE_LOOP(1);
 #undef DQ_SCALE_LOOP
 }
 
 struct MmLaunch {
   int split;    // CTAs of a cluster, each with its share of the K tiles
   int stages;   // ring slots
-  int unit_x, unit_w;  // bytes that a scale load may take: the alignment of pointer and row
+  int unit_x, unit_w;  // powers of two that divide the scales' address and row
+  int vec4;            // fours of outputs are aligned
 };
 
 template <int FMT, int BN>
@@ -344,13 +379,17 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     }
     mbar_init(&acc_full, 1);
     mbar_fence_init();
-    if (blockIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   }
   if (warp == 1) tc_alloc<1, G::kAlloc>(smem_u32(&tmem_base));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
+  float f1, f2;
+  tensor_factors(p, f1, f2);
 
   if (warp == 0) {
     if (elect_one()) {
@@ -399,14 +438,12 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     const bool of_w = (warp & 1) == 0;
     ScaleTurn t{(warp - 2) >> 1};
     scale_warp<false>(of_w ? l.unit_w : l.unit_x, t, F::kPiece, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
-                      p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, flags);
+                      p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, flags, 0u);
   }
   __syncwarp();
 
   // the finished tile: tensor-memory lane = feature, column = token
   const int tv = (int)min((int64_t)BN, p.T - t0);
-  float f1, f2;
-  tensor_factors(p, f1, f2);
   bool ok = true;
   if (warp >= 2) {
     ok = __all_sync(0xffffffffu, mm_wait(&acc_full, 0, flags));
@@ -451,9 +488,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         if (r < l.split) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
       const int64_t nn = n0 + 4 * (e & 31), at = (t0 + (e >> 5)) * p.N + nn;
       const float o[4] = {s.x * f1 * f2, s.y * f1 * f2, s.z * f1 * f2, s.w * f1 * f2};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (nn + i < p.N) y_store(p.y, p.y_dt, at + i, o[i]);
+      y_store4(p.y, p.y_dt, at, o, p.N - nn, l.vec4);
     }
     cluster_sync();
   } else {
@@ -497,8 +532,11 @@ struct PairGeo {
 struct PairLaunch {
   unsigned tiles_m, tiles_n, tiles;  // products of 2^31 at most
   int unit_x, unit_w;
-  int wide;  // rows of Y start at multiples of 32 bytes
+  int wide;   // rows of Y start at multiples of 32 bytes
+  int vec4;   // fours of outputs are aligned
+  int split;  // pairs of a cluster, each with its share of the K tiles of one tile
 };
+constexpr int kPartPitch = 260;  // floats of a partial tile's row in shared memory: conflict-free both ways
 
 // Tile order: bands of 8 token tiles, features within, so that the pairs at
 // work at one time share operands in L2.
@@ -507,15 +545,6 @@ __device__ __forceinline__ void pair_tile(const PairLaunch& l, unsigned i, int64
   const unsigned height = min(8u, l.tiles_m - band * 8), col = rest / height;
   m = band * 8 + (rest - col * height);
   n = col;
-}
-
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dt) {
-  uint32_t r;
-  if (dt == DT_BF16)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 __device__ __forceinline__ void st_global_32b(void* p, const uint32_t* v) {
@@ -574,9 +603,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
   unsigned char* scales = ring + kPairStages * G::kStage;
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank();
-  const unsigned pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-  const int nk = (int)((p.K + F::kTileK - 1) / F::kTileK);
+  const int in_cluster = (int)cluster_rank(), rank = in_cluster & 1, share = in_cluster >> 1;
+  const uint32_t leader = (uint32_t)in_cluster & ~1u;
+  const unsigned pair = blockIdx.x / (2 * l.split), pairs = gridDim.x / (2 * l.split);
+  const int all_k = (int)((p.K + F::kTileK - 1) / F::kTileK);
+  const int k0 = (int)((int64_t)all_k * share / l.split), k1 = (int)((int64_t)all_k * (share + 1) / l.split);
   const int64_t nb = p.K / F::kGroup;
   unsigned* flags = p.flags;
   if (threadIdx.x == 0) {
@@ -591,7 +622,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     mbar_init(&acc_full, 1);
     mbar_init(&acc_empty, 2 * kPairEpilogue);
     mbar_fence_init();
-    if (blockIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   }
   if (warp == 9) tc_alloc<2, 512>(smem_u32(&tmem_base));
   tc_fence_before();
@@ -599,7 +629,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   MmSlot at;
+  bool gave_up = false;
 
   if (warp == 8) {
     if (elect_one()) {
@@ -608,7 +642,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (unsigned i = pair; i < l.tiles && ok; i += pairs) {
         int64_t m, n;
         pair_tile(l, i, m, n);
-        for (int kt = 0; kt < nk; ++kt, ++issued) {
+        for (int kt = k0; kt < k1; ++kt, ++issued) {
           if (!(ok = mm_wait(&empty[at.slot], at.phase ^ 1, flags))) break;
           unsigned char* st = ring + at.slot * G::kStage;
           if (rank == 0) mbar_arrive_expect_tx(&full_t[at.slot], 2 * (G::kA + G::kB));
@@ -628,9 +662,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (unsigned i = pair; i < l.tiles && ok; i += pairs, turn ^= 1) {
         if (!(ok = mm_wait(&acc_empty, turn ^ 1, flags))) break;
         tc_fence_after();
-        for (int kt = 0; kt < nk; ++kt, set ^= 1) {
+        for (int kt = k0; kt < k1; ++kt, set ^= 1) {
           const int u = kt % F::kPiece;
-          if (u == 0 && !(ok = mm_wait(&full_s[piece & 1], (piece >> 1) & 1, flags))) break;
+          if ((u == 0 || kt == k0) && !(ok = mm_wait(&full_s[piece & 1], (piece >> 1) & 1, flags))) break;
           if (!(ok = mm_wait(&full_t[at.slot], at.phase, flags))) break;
           tc_fence_after();
           const uint32_t st = smem_u32(ring + at.slot * G::kStage);
@@ -647,12 +681,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tc_mma<FMT, 2>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(256, 256, F::byte(k)), ca + 4 * F::atom(k),
-                           cb + 8 * F::atom(k), kt > 0 || k > 0);
-          tc_commit<2>(&empty[at.slot]);
-          if (u == F::kPiece - 1 || kt == nk - 1) tc_commit<2>(&empty_s[piece++ & 1]);
+                           cb + 8 * F::atom(k), kt > k0 || k > 0);
+          tc_commit<2>(&empty[at.slot], leader);
+          if (u == F::kPiece - 1 || kt == k1 - 1) tc_commit<2>(&empty_s[piece++ & 1], leader);
           at.next(kPairStages);
         }
-        tc_commit<2>(&acc_full);
+        tc_commit<2>(&acc_full, leader);
       }
     }
   } else if (warp >= 10) {
@@ -664,9 +698,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int64_t m, n;
       pair_tile(l, i, m, n);
       ok = scale_warp<true>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
-                            of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, 0, nk,
+                            of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, k0, k1 - k0,
                             scales + (of_x ? 0 : 4096 + (block - 1) * 512), G::kScales, of_x ? 512 : 1024, full_s, empty_s,
-                            flags);
+                            flags, leader);
     }
   } else {
     float f1, f2_;
@@ -678,13 +712,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int64_t m, n;
       pair_tile(l, i, m, n);
       if (!__all_sync(0xffffffffu, mm_wait(&acc_full, turn, flags))) {
-        pair_give_up<OUT32>(p, l, i, pairs, rank, warp);
+        if (l.split > 1)
+          gave_up = true;
+        else
+          pair_give_up<OUT32>(p, l, i, pairs, rank, warp);
         break;
       }
       tc_fence_after();
       const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
       const int64_t t0 = m * 256 + rank * 128 + 32 * q, t = t0 + lane, nn = n * 256 + 128 * half;
-      if (!OUT32) {
+      if (l.split > 1) {  // the partial tile to the idle ring, joined below
+        float* part = reinterpret_cast<float*>(ring) + (32 * q + lane) * kPartPitch + 128 * half;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[32];
+          tc_load32(src + c, v);
+          tc_load_wait32(v);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(part + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
+      } else if (!OUT32) {
         uint32_t o[64];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -696,7 +744,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (c == 1) {  // everything is in registers: the next tile's multiply-adds may begin
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(&acc_empty, 0);
+            if (lane == 0) mbar_arrive_cluster(&acc_empty, leader);
           }
           if (FMT == FMT_NVFP4) {
             const f2 f = splat(f1);
@@ -730,7 +778,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (c == 3) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(&acc_empty, 0);
+            if (lane == 0) mbar_arrive_cluster(&acc_empty, leader);
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f1 * f2_);
@@ -747,6 +795,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   }
   __syncwarp();
+  if (l.split > 1) {
+    // each CTA joins and stores its share of the 128 rows that the pairs' CTAs of its rank hold, in pair order
+    if (__any_sync(0xffffffffu, gave_up))
+      for (int e = lane; e < 32 * 128; e += 32)  // a wait ran out: no number that looks like a result
+        reinterpret_cast<float*>(ring)[(32 * (warp & 3) + (e >> 7)) * kPartPitch + 128 * (warp >> 2) + (e & 127)] =
+            __uint_as_float(0x7FC00000u);
+    cluster_sync();
+    float f1, f2_;
+    tensor_factors(p, f1, f2_);
+    int64_t m, n;
+    pair_tile(l, pair, m, n);
+    const int rows = 128 / l.split;
+    const uint32_t part = smem_u32(ring);
+    for (int e = threadIdx.x; e < rows * 64; e += kPairThreads) {
+      const int row = share * rows + (e >> 6), col = 4 * (e & 63);
+      const int64_t t = m * 256 + rank * 128 + row, nn = n * 256 + col;
+      if (t >= p.T || nn >= p.N) continue;
+      float4 v[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < l.split) v[r] = ld_cluster_f4(part + 4 * (row * kPartPitch + col), 2 * r + rank);
+      float4 sum = v[0];
+#pragma unroll
+      for (int r = 1; r < 4; ++r)
+        if (r < l.split) sum.x += v[r].x, sum.y += v[r].y, sum.z += v[r].z, sum.w += v[r].w;
+      const float o[4] = {sum.x * f1 * f2_, sum.y * f1 * f2_, sum.z * f1 * f2_, sum.w * f1 * f2_};
+      y_store4(p.y, p.y_dt, t * p.N + nn, o, p.N - nn, l.vec4);
+    }
+  }
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still signal it or read its shared memory
   if (warp == 9) {
@@ -781,6 +858,11 @@ static int scale_unit(const unsigned char* s, int64_t nb) {
   return (int)(v & (~v + 1));
 }
 
+// Fours of neighbouring outputs start at multiples of their size.
+static bool vec4_rows(const MatmulProblem& p) {
+  return p.N % 4 == 0 && (uintptr_t)p.y % (p.y_dt == DT_F32 ? 16 : 8) == 0;
+}
+
 template <int FMT, int BN>
 static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   using G = MmGeo<FMT, BN>;
@@ -792,13 +874,15 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
   MmLaunch l;
   l.split = 1;
-  while (l.split < 8 && 2 * l.split <= nk && tiles * l.split < sms) l.split *= 2;
+  while (l.split < 8 && l.split < nk && tiles * (l.split + 1) <= sms) ++l.split;
   const int64_t per = (nk + l.split - 1) / l.split;
-  const int room = ((BN <= 64 ? 110 : 220) * 1024 - 2 * G::kScales) / G::kStage;
+  // one CTA an SM takes the shared memory of one, more tiles that of three
+  const int room = ((tiles * l.split <= sms ? 220 : 74) * 1024 - 2 * G::kScales - 1024) / G::kStage;
   l.stages = (int)(per < room ? per : room);
   if (l.stages > kMmMaxStages) l.stages = kMmMaxStages;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
+  l.vec4 = vec4_rows(p);
   // the partial tile shares the ring's memory
   int smem = l.stages * G::kStage + 2 * G::kScales;
   if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
@@ -815,23 +899,11 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   if (smem < share) smem = share;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(tiles * l.split));
-  cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)l.split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, l, wmap, xmap);
+  return launch_early(kern, (unsigned)(tiles * l.split), kMmThreads, (size_t)smem, l.split, st, p, l, wmap, xmap);
 }
 
 template <int FMT, bool OUT32>
-static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st) {
+static cudaError_t matmul_pair(const MatmulProblem& p, int split, int sms, cudaStream_t st) {
   using G = PairGeo<FMT>;
   CUtensorMap wmap, xmap;
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
@@ -847,20 +919,10 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
   auto kern = k_matmul_pair<FMT, OUT32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned pairs = l.tiles < (unsigned)sms / 2 ? l.tiles : (unsigned)sms / 2;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(kPairThreads);
-  cfg.dynamicSmemBytes = (size_t)G::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p, l, wmap, xmap);
+  l.vec4 = vec4_rows(p);
+  l.split = split;
+  const unsigned pairs = split > 1 ? l.tiles * split : (l.tiles < (unsigned)sms / 2 ? l.tiles : (unsigned)sms / 2);
+  return launch_early(kern, 2 * pairs, kPairThreads, (size_t)G::kSmem, 2 * split, st, p, l, wmap, xmap);
 }
 
 template <int FMT>
@@ -870,8 +932,10 @@ static cudaError_t matmul_fmt(const MatmulProblem& p, int sms, cudaStream_t st) 
   if (p.T <= 16) return matmul_tc<FMT, 16>(p, sms, st);
   if (p.T <= 32) return matmul_tc<FMT, 32>(p, sms, st);
   if (p.T <= 64) return matmul_tc<FMT, 64>(p, sms, st);
-  if (p.T <= 128 || (p.N + 255) / 256 * ((p.T + 255) / 256) < sms / 4) return matmul_tc<FMT, 128>(p, sms, st);
-  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, sms, st) : matmul_pair<FMT, false>(p, sms, st);
+  const int64_t tiles = (p.N + 255) / 256 * ((p.T + 255) / 256);
+  const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
+  const int split = tiles * 4 <= sms / 4 && nk >= 8 ? 4 : (tiles * 2 <= sms / 2 && nk >= 8 ? 2 : 1);
+  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, split, sms, st) : matmul_pair<FMT, false>(p, split, sms, st);
 }
 
 }  // namespace dq

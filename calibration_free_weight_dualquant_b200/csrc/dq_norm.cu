@@ -28,6 +28,7 @@
 #include "dq_device.cuh"
 #include "dq_fast.cuh"
 #include "dq_internal.h"
+#include "dq_launch.h"
 
 namespace dq {
 
@@ -340,8 +341,11 @@ __device__ __forceinline__ void row_grid_barrier(WsHeader* hdr) {
   __syncthreads();
 }
 
-// A grid of one CTA clears its own header.
-__device__ __forceinline__ void row_clear_header(WsHeader* hdr) {
+// Start of a kernel: everything before it in the stream is done.  A grid of one
+// CTA clears its own header.
+__device__ __forceinline__ void row_begin(WsHeader* hdr) {
+  griddep_launch_dependents();
+  griddep_wait();
   if (gridDim.x == 1) {
     if (threadIdx.x == 0) {
       hdr->flags = 0;
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
   const int chunks = (int)(p.K / 16);
   const int trips = NC > 0 ? 1 : (chunks + nt - 1) / nt;
   const void* hsrc = p.y ? p.h : p.x;
-  row_clear_header(p.hdr);
+  row_begin(p.hdr);
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
@@ -641,7 +645,7 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu(const __grid_constant__ 
   // ... and as elements of the inputs and outputs, without and with a carry into the next row
   const int64_t din = drow * p.ld + dspan * 512, dout = drow * p.K + dspan * 512;
   const int64_t cin = p.ld - spans * 512, cout = p.K - spans * 512;
-  row_clear_header(p.hdr);
+  row_begin(p.hdr);
   double amax = 0.0;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
@@ -730,10 +734,8 @@ static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, boo
     grid = (int)(want < most ? want : most);
   }
   if (grid > 1 && (e = cudaMemsetAsync(p.hdr, 0, sizeof(WsHeader), st)) != cudaSuccess) return e;
-  if (!coop || grid == 1) {
-    kern<<<grid, threads, smem, st>>>(p);
-    return cudaGetLastError();
-  }
+  if (!coop || grid == 1)
+    return launch_early(kern, (unsigned)grid, (unsigned)threads, smem, 1, st, p);
   RowProblem arg = p;
   void* args[] = {&arg};
   return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(threads), args, smem, st);

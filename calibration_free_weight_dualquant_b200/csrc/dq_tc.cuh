@@ -107,16 +107,17 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 #undef DQ_TC_MMA
 
-// Arrives on `bar` (of a pair: on both CTAs' barriers at that place) when
-// everything this thread issued to the tensor core is done.
+// Arrives on `bar` (of a pair whose even CTA has the cluster rank `leader`: on
+// both CTAs' barriers at that place) when everything this thread issued to the
+// tensor core is done.
 template <int CG>
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t leader = 0) {
   if (CG == 1)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
   else
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
                      smem_u32(bar)),
-                 "h"((uint16_t)3)
+                 "h"((uint16_t)(3u << leader))
                  : "memory");
 }
 
