@@ -347,6 +347,7 @@ struct MmLaunch {
   int stages;   // ring slots
   int unit_x, unit_w;  // powers of two that divide the scales' address and row
   int vec4;            // fours of outputs are aligned
+  int early;           // the next grid may begin from the start on (else from the end of the multiply-adds on)
 };
 
 template <int FMT, int BN>
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  griddep_launch_dependents();
+  if (l.early) griddep_launch_dependents();
   griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   float f1, f2;
@@ -441,6 +442,8 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                       p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, flags, 0u);
   }
   __syncwarp();
+
+  if (!l.early) griddep_launch_dependents();
 
   // the finished tile: tensor-memory lane = feature, column = token
   const int tv = (int)min((int64_t)BN, p.T - t0);
@@ -876,13 +879,15 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   l.split = 1;
   while (l.split < 8 && l.split < nk && tiles * (l.split + 1) <= sms) ++l.split;
   const int64_t per = (nk + l.split - 1) / l.split;
-  // one CTA an SM takes the shared memory of one, more tiles that of three
+  // one CTA an SM takes all shared memory, more tiles share an SM by three
   const int room = ((tiles * l.split <= sms ? 220 : 74) * 1024 - 2 * G::kScales - 1024) / G::kStage;
   l.stages = (int)(per < room ? per : room);
   if (l.stages > kMmMaxStages) l.stages = kMmMaxStages;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
   l.vec4 = vec4_rows(p);
+  // where an SM takes several CTAs, those of the next grid would take the places of this one unevenly
+  l.early = tiles * l.split <= sms;
   // the partial tile shares the ring's memory
   int smem = l.stages * G::kStage + 2 * G::kScales;
   if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;

@@ -32,7 +32,8 @@
 
 namespace dq {
 
-constexpr int kGluThreads = 256;
+constexpr int kGluThreads = 256;   // dq_glu_quant's block; two an SM
+constexpr int kGluMax = 512;       // ... and of a call that one CTA takes
 constexpr float kFltMax = 3.402823466e38f;
 
 struct RowProblem {
@@ -364,14 +365,6 @@ __device__ __forceinline__ float tensor_scale(unsigned long long bits) {
   return s == 0.f ? 0x1p-149f : s;
 }
 
-// Block-wide maximum of a non-negative double into hdr->amax_scaled.
-__device__ __forceinline__ void amax_to_header(WsHeader* hdr, double amax) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0 && amax > 0.0)
-    atomicMax(&hdr->amax_scaled, (unsigned long long)__double_as_longlong(amax));
-}
-
 // ---------------------------------------------------------------------------
 // dq_norm_quant: a CTA takes rows grid-stride, thread t the 16-element chunks
 // t, t + blockDim, ...  With NC > 0 a thread has at most NC chunks and keeps its
@@ -413,32 +406,73 @@ __device__ __forceinline__ double row_rstd(double s, double* red, const RowProbl
   return red[32];
 }
 
-// Raises amax to the largest finite |x'| of the 512 elements whose lanes ask for
-// it, in fp64, an element a lane; every lane of the warp calls it.
+// The tensor's amax (NVFP4), exact without fp64 for every element: a lane keeps
+// the chunk with its largest fp32 maximum (a relative 2^-20 off) and at the end
+// the CTA's largest are evaluated in fp64.  Chunks within 2^-18 of the lane's
+// largest, and those about which the fp32 value says nothing (a NaN, an
+// infinity, an underflow), are evaluated when they come.
+struct Amax {
+  double exact = 0.0;  // of the chunks evaluated so far
+  float best = 0.f;
+  int64_t at = 0;      // first element of the lane's best chunk
+  double rstd = 0.0;   // its row's
+};
+
+// Raises a.exact to the largest finite |x'| of the 16-element chunks from `at`
+// of the lanes in the mask, an element a lane; every lane of the warp calls it.
 template <int XDT, bool GLU>
 static __device__ __noinline__ double amax_exact(const RowProblem& p, int64_t at, uint32_t lanes, double rstd, double amax) {
   const int lane = threadIdx.x & 31;
   for (uint32_t rest = lanes; rest != 0; rest &= rest - 1) {
-    const int64_t first = __shfl_sync(0xffffffffu, at, __ffs(rest) - 1), row = first / p.K;
-    const double x = lane < 16 ? fabs(exact1<XDT, GLU>(p, row, first - row * p.K + lane, rstd)) : 0.0;
+    const int from = __ffs(rest) - 1;
+    const int64_t first = __shfl_sync(0xffffffffu, at, from), row = first / p.K;
+    const double r = __shfl_sync(0xffffffffu, rstd, from);
+    const double x = lane < 16 ? fabs(exact1<XDT, GLU>(p, row, first - row * p.K + lane, r)) : 0.0;
     if (x <= (double)kFltMax) amax = fmax(amax, x);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   return amax;
 }
 
-// Lanes whose fp32 maximum m (a relative 2^-20 off) could raise the warp's amax.
-// Of those, only the ones next to the largest m of them.
-__device__ __forceinline__ uint32_t amax_lanes(float m, bool on, bool force, double amax) {
-  const bool could = on && (force || !((double)m * (1.0 + 0x1p-18) < amax) || (m < 0x1p-60f && amax < 0x1p-59));
-  if (!__any_sync(0xffffffffu, could)) return 0;
-  // a NaN, an infinity or a tiny value says nothing about the others
-  const bool plain = could && !force && m >= 0x1p-60f && m <= kFltMax;
-  float top = plain ? m : 0.f;
+template <int XDT, bool GLU>
+__device__ __forceinline__ void amax_add(const RowProblem& p, Amax& a, float m, int64_t at, bool on, bool force, double rstd) {
+  const bool plain = !force && m >= 0x1p-60f && m <= kFltMax;
+  bool now = on && !plain;
+  if (on && plain) {
+    if (m > a.best * (1.f + 0x1p-18f)) {
+      a.best = m;
+      a.at = at;
+      a.rstd = rstd;
+    } else {
+      now = m >= a.best * (1.f - 0x1p-18f);
+    }
+  }
+  const uint32_t ask = __ballot_sync(0xffffffffu, now);
+  if (ask) a.exact = amax_exact<XDT, GLU>(p, at, ask, rstd, a.exact);
+}
+
+// The call's amax from the threads' shares (bits of a double; a wait for the
+// other CTAs that runs out sets the header's flag).
+template <int XDT, bool GLU>
+__device__ __forceinline__ unsigned long long amax_finish(const RowProblem& p, Amax& a) {
+  __shared__ unsigned top;  // fp32 bits: positive floats order as integers
+  __shared__ unsigned long long all;
+  if (threadIdx.x == 0) top = 0, all = 0;
+  __syncthreads();
+  float m = a.best;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  return __ballot_sync(0xffffffffu, could && !(plain && m * (1.f + 0x1p-18f) < top));
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) atomicMax(&top, __float_as_uint(m));
+  __syncthreads();
+  const uint32_t ask = __ballot_sync(0xffffffffu, a.best > 0.f && a.best >= __uint_as_float(top) * (1.f - 0x1p-18f));
+  if (ask) a.exact = amax_exact<XDT, GLU>(p, a.at, ask, a.rstd, a.exact);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a.exact = fmax(a.exact, __shfl_xor_sync(0xffffffffu, a.exact, o));
+  if ((threadIdx.x & 31) == 0 && a.exact > 0.0) atomicMax(&all, (unsigned long long)__double_as_longlong(a.exact));
+  __syncthreads();
+  if (gridDim.x == 1) return all;
+  if (threadIdx.x == 0) atomicMax(&p.hdr->amax_scaled, all);
+  row_grid_barrier(p.hdr);
+  return *reinterpret_cast<volatile unsigned long long*>(&p.hdr->amax_scaled);
 }
 
 __host__ __device__ constexpr int norm_threads(int nc) { return nc == 1 ? 512 : 256; }
@@ -454,7 +488,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
   const int trips = NC > 0 ? 1 : (chunks + nt - 1) / nt;
   const void* hsrc = p.y ? p.h : p.x;
   row_begin(p.hdr);
-  double amax = 0.0;
+  Amax amax;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
   V16 hv[N], rv[N];  // zeros for good where the thread has no chunk
@@ -484,10 +518,8 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
 #pragma unroll 1
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
     if (FMT == FMT_NVFP4 && pass == 1) {
-      amax_to_header(p.hdr, amax);
-      row_grid_barrier(p.hdr);
+      sT = tensor_scale(amax_finish<XDT, false>(p, amax));
       if (ld_volatile(&p.hdr->flags) & kFlagTimeout) return;
-      sT = tensor_scale(*reinterpret_cast<volatile unsigned long long*>(&p.hdr->amax_scaled));
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
@@ -557,9 +589,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
           for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], splat(rs)), gb[i]);
           if (FMT == FMT_NVFP4 && pass == 0) {
             // values that are not finite have no share in the tensor scale
-            const float mf = absmax16(v);
-            const uint32_t ask = amax_lanes(mf, on && rstd == rstd, !rs_ok, amax);
-            if (ask) amax = amax_exact<XDT, false>(p, row0 + i0 * 16, ask, rstd, amax);
+            amax_add<XDT, false>(p, amax, absmax16(v), row0 + i0 * 16, on && rstd == rstd && !zero_bits16(hv[c]), !rs_ok, rstd);
           } else {
             // relative error: 1/rms, two products, the scale's factor and the scaled value, 2^-24 each (NVFP4: three more)
             bad |= quant_store16<FMT, XDT, false>(p, row0 + i0 * 16, on, v, 0x1p-20f, sT, isT, [&] { return zero_bits16(hv[c]); },
@@ -635,18 +665,18 @@ __device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const f
 }
 
 template <int FMT, int XDT>
-__global__ void __launch_bounds__(kGluThreads, 2) k_glu(const __grid_constant__ RowProblem p) {
+__global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowProblem p) {
   const int lane = threadIdx.x & 31;
   const int64_t spans = (p.K + 511) / 512;  // 512-column pieces of a row
-  const int64_t w0 = (int64_t)blockIdx.x * (kGluThreads / 32) + (threadIdx.x >> 5);
-  const int64_t all = (int64_t)gridDim.x * (kGluThreads / 32);
+  const int64_t w0 = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t all = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int64_t nw = all >= spans ? all / spans * spans : all;  // warps that take items
   const int drow = (int)(nw / spans), dspan = (int)(nw - drow * spans);  // the grid's stride as rows and spans
   // ... and as elements of the inputs and outputs, without and with a carry into the next row
   const int64_t din = drow * p.ld + dspan * 512, dout = drow * p.K + dspan * 512;
   const int64_t cin = p.ld - spans * 512, cout = p.K - spans * 512;
   row_begin(p.hdr);
-  double amax = 0.0;
+  Amax amax;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
   f2 b[8];
@@ -654,10 +684,8 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu(const __grid_constant__ 
 #pragma unroll 1
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
     if (FMT == FMT_NVFP4 && pass == 1) {
-      amax_to_header(p.hdr, amax);
-      row_grid_barrier(p.hdr);
+      sT = tensor_scale(amax_finish<XDT, true>(p, amax));
       if (ld_volatile(&p.hdr->flags) & kFlagTimeout) return;
-      sT = tensor_scale(*reinterpret_cast<volatile unsigned long long*>(&p.hdr->amax_scaled));
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
@@ -699,8 +727,7 @@ __global__ void __launch_bounds__(kGluThreads, 2) k_glu(const __grid_constant__ 
       glu_fast16<XDT>(gv, uv, b, v, far);
       if (FMT == FMT_NVFP4 && pass == 0) {
         // values that are not finite have no share in the tensor scale
-        const uint32_t ask = amax_lanes(absmax16(v), on, far, amax);
-        if (ask) amax = amax_exact<XDT, true>(p, here, ask, 0.0, amax);
+        amax_add<XDT, true>(p, amax, absmax16(v), here, on && !zero_bits16(gv) && !zero_bits16(uv), far, 0.0);
       } else {
         // 2^-21 of x' and the roundings of the scaled value
         bad |= quant_store16<FMT, XDT, true>(p, here, on, v, 1.25f * 0x1p-20f, sT, isT,
@@ -765,6 +792,8 @@ static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
 template <int FMT, int XDT>
 static cudaError_t glu_launch(const RowProblem& p, int sms, cudaStream_t st) {
   const int64_t items = p.M * ((p.K + 511) / 512);
+  // NVFP4, few items: one CTA, whose two passes need no grid barrier and whose header no clearing
+  if (FMT == FMT_NVFP4 && items <= 2 * (kGluMax / 32)) return row_launch(k_glu<FMT, XDT>, p, true, 1, kGluMax, 0, sms, st);
   return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, 0, sms, st);
 }
 
