@@ -361,8 +361,9 @@ def dq_act_quant(X: torch.Tensor, col_scales: torch.Tensor, fmt, group: Optional
 def _call(device: torch.device, stream, f, *args):
     """f(stream pointer, ...) with the device of the call's tensors as the current one, and ``stream`` (default:
     that device's current stream) as the stream that new outputs and workspaces belong to."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return f(torch._C._cuda_getCurrentRawStream(device.index), *args)
+    index = device.index
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return f(torch._C._cuda_getCurrentRawStream(index), *args)
     with torch.cuda.device(device):
         if stream is None:
             return f(torch.cuda.current_stream().cuda_stream, *args)
@@ -371,27 +372,23 @@ def _call(device: torch.device, stream, f, *args):
 
 
 def _quantized(t: dict, f: Format, device, where: str) -> tuple:
-    """(rows, cols) of a quantized matrix {"codes", "block_scales", "tensor_scale"}; DQError unless its tensors
-    are the format's, on `device`."""
+    """(rows, cols, struct) of a quantized matrix {"codes", "block_scales", "tensor_scale"}; DQError unless its
+    tensors are the format's, on `device`."""
     codes, scales = t["codes"], t["block_scales"]
-    if codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_contiguous() or codes.device != device:
+    if codes.dim() != 2 or codes.dtype is not torch.uint8 or not codes.is_contiguous() or codes.device != device:
         raise DQError(1, where + ": codes must be a contiguous 2-D uint8 tensor on the call's device")
     r, c = codes.shape
-    if f != Format.MXFP8:
+    if f is not Format.MXFP8:
         c *= 2
-    if (scales.dtype != torch.uint8 or not scales.is_contiguous() or scales.device != device
+    if (scales.dtype is not torch.uint8 or not scales.is_contiguous() or scales.device != device
             or scales.shape != (r, c // DEFAULT_GROUP[f])):
         raise DQError(1, where + ": block_scales must be contiguous uint8 [rows][cols/group] on the call's device")
-    if f == Format.NVFP4:
-        s = t.get("tensor_scale")
-        if s is None or s.dtype != torch.float32 or s.numel() != 1 or s.device != device:
-            raise DQError(1, where + ": NVFP4 needs a one-element float32 tensor_scale on the call's device")
-    return r, c
-
-
-def _quantized_struct(t: dict, f: Format) -> _Outputs:
-    return _Outputs(t["codes"].data_ptr(), t["block_scales"].data_ptr(),
-                    t["tensor_scale"].data_ptr() if f == Format.NVFP4 else None, None, None)
+    if f is not Format.NVFP4:
+        return r, c, _Outputs(codes.data_ptr(), scales.data_ptr())
+    s = t.get("tensor_scale")
+    if s is None or s.dtype is not torch.float32 or s.numel() != 1 or s.device != device:
+        raise DQError(1, where + ": NVFP4 needs a one-element float32 tensor_scale on the call's device")
+    return r, c, _Outputs(codes.data_ptr(), scales.data_ptr(), s.data_ptr())
 
 
 _PRODUCT_FORMATS = {k: f for f in (Format.NVFP4, Format.MXFP4, Format.MXFP8) for k in (f, int(f), f.name.lower())}
@@ -407,9 +404,13 @@ def _product_format(fmt, group: Optional[int], where: str) -> Format:
     return f
 
 
-def _check_workspace(workspace: torch.Tensor, device, where: str):
-    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+def _workspace(workspace: Optional[torch.Tensor], codes: torch.Tensor, nbytes: int, where: str) -> tuple:
+    """(the workspace tensor or None, its bytes): the caller's, or a new one of nbytes next to `codes`."""
+    if workspace is None:
+        return (codes.new_empty(nbytes), nbytes) if nbytes else (None, 0)
+    if workspace.device != codes.device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise DQError(1, where + ": workspace must be a contiguous uint8 tensor on the call's device")
+    return workspace, workspace.numel()
 
 
 def _raise_device_status(workspace: torch.Tensor, stream_ptr: int, where: str):
@@ -440,8 +441,8 @@ def dq_matmul(X: dict, W: dict, fmt, group: Optional[int] = None, out: Optional[
 
 def _matmul(sp, codes, X, W, f, out, out_dtype, workspace, check):
     dev = codes.device
-    tokens, cols = _quantized(X, f, dev, "dq_matmul: X")
-    rows, wcols = _quantized(W, f, dev, "dq_matmul: W")
+    tokens, cols, xs = _quantized(X, f, dev, "dq_matmul: X")
+    rows, wcols, ws = _quantized(W, f, dev, "dq_matmul: W")
     if wcols != cols:
         raise DQError(1, "dq_matmul: W has %d columns and X %d" % (wcols, cols))
     if out is None:
@@ -450,29 +451,32 @@ def _matmul(sp, codes, X, W, f, out, out_dtype, workspace, check):
         out = codes.new_empty((tokens, rows), dtype=out_dtype)
     elif out.dtype not in _DTYPES or out.shape != (tokens, rows) or not out.is_contiguous() or out.device != dev:
         raise DQError(1, "dq_matmul: out must be contiguous f32/bf16/f16 [tokens, rows] on the call's device")
-    if workspace is not None:
-        _check_workspace(workspace, dev, "dq_matmul")
-    elif check:
-        workspace = codes.new_empty(MATMUL_WORKSPACE_BYTES)
-    st = _lib.dq_matmul(_quantized_struct(X, f), tokens, _quantized_struct(W, f), rows, cols, f, DEFAULT_GROUP[f],
-                        out.data_ptr(), _DTYPES[out.dtype], None if workspace is None else workspace.data_ptr(),
-                        0 if workspace is None else workspace.numel(), sp)
+    wp, wn = _workspace(workspace, codes, MATMUL_WORKSPACE_BYTES if check else 0, "dq_matmul")
+    st = _lib.dq_matmul(xs, tokens, ws, rows, cols, f, DEFAULT_GROUP[f], out.data_ptr(), _DTYPES[out.dtype],
+                        None if wp is None else wp.data_ptr(), wn, sp)
     if st != 0:
         raise DQError(st, "dq_matmul")
     if check:
-        _raise_device_status(workspace, sp, "dq_matmul")
+        _raise_device_status(wp, sp, "dq_matmul")
     return out
 
 
-def _row_outputs(out: Optional[dict], like: torch.Tensor, rows: int, cols: int, f: Format, where: str) -> dict:
-    if out is None:
-        out = {"codes": like.new_empty((rows, cols if f == Format.MXFP8 else cols // 2), dtype=torch.uint8),
-               "block_scales": like.new_empty((rows, cols // DEFAULT_GROUP[f]), dtype=torch.uint8)}
-        if f == Format.NVFP4:
-            out["tensor_scale"] = like.new_empty(1, dtype=torch.float32)
-    elif _quantized(out, f, like.device, where) != (rows, cols):
-        raise DQError(1, where + " must be [%d][%d columns]" % (rows, cols))
-    return out
+def _row_outputs(out: Optional[dict], like: torch.Tensor, rows: int, cols: int, f: Format, where: str) -> tuple:
+    """(the output dict, its struct)."""
+    if out is not None:
+        r, c, struct = _quantized(out, f, like.device, where)
+        if r != rows or c != cols:
+            raise DQError(1, where + " must be [%d][%d columns]" % (rows, cols))
+        return out, struct
+    if cols % DEFAULT_GROUP[f] != 0:
+        raise DQError(1, where + ": %d columns are not a multiple of the group" % cols)
+    codes = like.new_empty((rows, cols if f is Format.MXFP8 else cols // 2), dtype=torch.uint8)
+    scales = codes.new_empty((rows, cols // DEFAULT_GROUP[f]))
+    if f is not Format.NVFP4:
+        return {"codes": codes, "block_scales": scales}, _Outputs(codes.data_ptr(), scales.data_ptr())
+    s = like.new_empty(1, dtype=torch.float32)
+    return ({"codes": codes, "block_scales": scales, "tensor_scale": s},
+            _Outputs(codes.data_ptr(), scales.data_ptr(), s.data_ptr()))
 
 
 def _channel_vector(t: torch.Tensor, cols: int, dtypes, device, where: str) -> int:
@@ -491,7 +495,7 @@ def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: O
     """Enqueue dq_norm_quant: h = X + residual (if given), its RMS norm times ``weight`` and the column inverse
     scales, quantized row-wise in ``fmt`` (mxfp8, mxfp4 or nvfp4).  Returns the quantized matrix with
     out["residual"] = h (with a residual; ``residual_out`` may be X or the residual itself).  A non-finite row
-    gets NaN scales; ``check`` waits and raises on it."""
+    gets NaN scales; ``check`` waits and raises on it, and a ``workspace`` reports it later without that."""
     load_library()
     f = _product_format(fmt, group, "dq_norm_quant")
     if not X.is_cuda or X.dtype not in _HALVES or not X.is_contiguous() or X.dim() != 2:
@@ -511,24 +515,23 @@ def _norm_quant(sp, X, weight, col_scales, f, residual, eps, out, residual_out, 
     gp = None if weight is None else _channel_vector(weight, cols, (X.dtype,), dev,
                                                      "dq_norm_quant: weight (in X's dtype)")
     bp = None if col_scales is None else _channel_vector(col_scales, cols, _HALVES, dev, "dq_norm_quant: col_scales")
-    out = _row_outputs(out, X, rows, cols, f, "dq_norm_quant: out")
+    out, struct = _row_outputs(out, X, rows, cols, f, "dq_norm_quant: out")
     if residual is not None and residual_out is None:
         residual_out = X.new_empty((rows, cols))
-    if workspace is None:
-        workspace = X.new_empty(ACT_WORKSPACE_BYTES + (8 * rows if f == Format.NVFP4 else 0), dtype=torch.uint8)
-    else:
-        _check_workspace(workspace, dev, "dq_norm_quant")
+    need = ACT_WORKSPACE_BYTES + 8 * rows if f is Format.NVFP4 else (ACT_WORKSPACE_BYTES if check else 0)
+    workspace, wn = _workspace(workspace, out["codes"], need, "dq_norm_quant")
     st = _lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), _DTYPES[X.dtype], rows, cols,
                             gp, eps, bp, 1 if col_scales is None else _DTYPES[col_scales.dtype], f, DEFAULT_GROUP[f],
-                            _quantized_struct(out, f), None if residual is None else residual_out.data_ptr(),
-                            workspace.data_ptr(), workspace.numel(), sp)
+                            struct, None if residual is None else residual_out.data_ptr(),
+                            None if workspace is None else workspace.data_ptr(), wn, sp)
     if st != 0:
         raise DQError(st, "dq_norm_quant")
     if check:
         _raise_device_status(workspace, sp, "dq_norm_quant")
     if residual is not None:
         out["residual"] = residual_out
-    out["workspace"] = workspace
+    if workspace is not None:
+        out["workspace"] = workspace
     return out
 
 
@@ -561,19 +564,18 @@ def _glu_quant(sp, gate, up, one, col_scales, f, out, workspace, check):
     ld = gate.stride(0) if rows > 1 else cols + (-cols % 8)
     bp = None if col_scales is None else _channel_vector(col_scales, cols, _HALVES, gate.device,
                                                          "dq_glu_quant: col_scales")
-    out = _row_outputs(out, gate, rows, cols, f, "dq_glu_quant: out")
-    if workspace is None:
-        workspace = gate.new_empty(ACT_WORKSPACE_BYTES, dtype=torch.uint8)
-    else:
-        _check_workspace(workspace, gate.device, "dq_glu_quant")
+    out, struct = _row_outputs(out, gate, rows, cols, f, "dq_glu_quant: out")
+    workspace, wn = _workspace(workspace, out["codes"], ACT_WORKSPACE_BYTES if check or f is Format.NVFP4 else 0,
+                               "dq_glu_quant")
     st = _lib.dq_glu_quant(gp, upp, _DTYPES[gate.dtype], rows, cols, ld, bp,
-                           1 if col_scales is None else _DTYPES[col_scales.dtype], f, DEFAULT_GROUP[f],
-                           _quantized_struct(out, f), workspace.data_ptr(), workspace.numel(), sp)
+                           1 if col_scales is None else _DTYPES[col_scales.dtype], f, DEFAULT_GROUP[f], struct,
+                           None if workspace is None else workspace.data_ptr(), wn, sp)
     if st != 0:
         raise DQError(st, "dq_glu_quant")
     if check:
         _raise_device_status(workspace, sp, "dq_glu_quant")
-    out["workspace"] = workspace
+    if workspace is not None:
+        out["workspace"] = workspace
     return out
 
 

@@ -347,7 +347,7 @@ __device__ __forceinline__ void row_grid_barrier(WsHeader* hdr) {
 __device__ __forceinline__ void row_begin(WsHeader* hdr) {
   griddep_launch_dependents();
   griddep_wait();
-  if (gridDim.x == 1) {
+  if (gridDim.x == 1 && hdr) {
     if (threadIdx.x == 0) {
       hdr->flags = 0;
       hdr->gbar = 0;
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
     }
   }
   if (blockIdx.x == 0 && tid == 0 && p.sT_out) *p.sT_out = sT;
-  if (bad && (tid & 31) == 0) atomicOr(&p.hdr->flags, kFlagNonFinite);
+  if (bad && (tid & 31) == 0 && p.hdr) atomicOr(&p.hdr->flags, kFlagNonFinite);
 }
 
 // ---------------------------------------------------------------------------
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.sT_out) *p.sT_out = sT;
-  if (bad && lane == 0) atomicOr(&p.hdr->flags, kFlagNonFinite);
+  if (bad && lane == 0 && p.hdr) atomicOr(&p.hdr->flags, kFlagNonFinite);
 }
 
 // ---------------------------------------------------------------------------
@@ -760,7 +760,7 @@ static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, boo
     const int64_t most = (int64_t)sms * per_sm;
     grid = (int)(want < most ? want : most);
   }
-  if (grid > 1 && (e = cudaMemsetAsync(p.hdr, 0, sizeof(WsHeader), st)) != cudaSuccess) return e;
+  if (grid > 1 && p.hdr && (e = cudaMemsetAsync(p.hdr, 0, sizeof(WsHeader), st)) != cudaSuccess) return e;
   if (!coop || grid == 1)
     return launch_early(kern, (unsigned)grid, (unsigned)threads, smem, 1, st, p);
   RowProblem arg = p;
@@ -811,7 +811,7 @@ static int row_check(int64_t rows, int64_t cols, int x_dtype, const void* col_sc
   if (!out || !out->codes || !out->block_scales || (uintptr_t)out->codes % 8 != 0 ||
       (format == DQ_NVFP4 && !out->tensor_scale) || (uintptr_t)out->tensor_scale % 4 != 0)
     return DQ_EINVAL;
-  if (!workspace || (uintptr_t)workspace % 256 != 0) return DQ_EINVAL;
+  if ((!workspace && format == DQ_NVFP4) || (uintptr_t)workspace % 256 != 0) return DQ_EINVAL;
   return DQ_OK;
 }
 
@@ -853,7 +853,7 @@ extern "C" int dq_norm_quant(const void* X, const void* residual, int x_dtype, i
   if (!X || (uintptr_t)X % 16 != 0 || (uintptr_t)residual % 16 != 0 || (uintptr_t)weight % 16 != 0) return DQ_EINVAL;
   if (residual ? (!residual_out || (uintptr_t)residual_out % 16 != 0) : residual_out != nullptr) return DQ_EINVAL;
   if (!(eps >= 0.f && eps <= dq::kFltMax)) return DQ_EINVAL;
-  if (workspace_bytes < dq_norm_workspace_bytes(rows, cols, format, group)) return DQ_EWORKSPACE;
+  if (workspace && workspace_bytes < dq_norm_workspace_bytes(rows, cols, format, group)) return DQ_EWORKSPACE;
   int sms = 0;
   if ((st = dq::row_sms(&sms)) != DQ_OK) return st;
   dq::RowProblem p{};
@@ -865,7 +865,7 @@ extern "C" int dq_norm_quant(const void* X, const void* residual, int x_dtype, i
   p.eps = eps;
   p.h = residual_out;
   p.wide = ((uintptr_t)X | (uintptr_t)residual | (uintptr_t)residual_out) % 32 == 0;  // a row is a multiple of 32 bytes
-  p.rstd = reinterpret_cast<double*>(static_cast<unsigned char*>(workspace) + DQ_ACT_WORKSPACE_BYTES);
+  if (format == DQ_NVFP4) p.rstd = reinterpret_cast<double*>(static_cast<unsigned char*>(workspace) + DQ_ACT_WORKSPACE_BYTES);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (format == DQ_NVFP4)
@@ -884,7 +884,7 @@ extern "C" int dq_glu_quant(const void* gate, const void* up, int x_dtype, int64
   if (st != DQ_OK) return st;
   if (!gate || !up || (uintptr_t)gate % 16 != 0 || (uintptr_t)up % 16 != 0) return DQ_EINVAL;
   if (ld < cols || ld % 8 != 0 || rows > ((int64_t)1 << 40) / ld) return DQ_EINVAL;
-  if (workspace_bytes < DQ_ACT_WORKSPACE_BYTES) return DQ_EWORKSPACE;
+  if (workspace && workspace_bytes < DQ_ACT_WORKSPACE_BYTES) return DQ_EWORKSPACE;
   int sms = 0;
   if ((st = dq::row_sms(&sms)) != DQ_OK) return st;
   dq::RowProblem p{};

@@ -348,7 +348,8 @@ size_t dq_norm_workspace_bytes(int64_t rows, int64_t cols, int format, int group
  * A value of x' that is NaN or beyond fp32's range gives its group the format's
  * NaN scale (E8M0 0xFF, E4M3 0x7F) and zero codes, takes no part in the tensor
  * scale, and dq_sync_status reports DQ_ENONFINITE; every other group is valid.
- * A NaN or an infinity in h makes its whole row such.
+ * A NaN or an infinity in h makes its whole row such.  The workspace may be NULL
+ * for the MX formats: the scales alone tell then.
  * X, residual, residual_out and weight 16-byte aligned, codes 8-byte aligned. */
 int dq_norm_quant(const void* X, const void* residual, int x_dtype, int64_t rows, int64_t cols, const void* weight,
                   float eps, const void* col_scales, int col_dtype, int format, int group, const dq_outputs* out,
@@ -362,7 +363,7 @@ int dq_norm_quant(const void* X, const void* residual, int x_dtype, int64_t rows
  * DQ_F16) share the row stride `ld` in elements (ld >= cols, a multiple of 8):
  * the two halves of one product's output [rows][2 cols] are gate, gate + cols
  * and ld = 2 cols.  Both 16-byte aligned, codes 8-byte aligned; workspace
- * DQ_ACT_WORKSPACE_BYTES, 256-byte aligned. */
+ * DQ_ACT_WORKSPACE_BYTES, 256-byte aligned, or NULL for the MX formats. */
 int dq_glu_quant(const void* gate, const void* up, int x_dtype, int64_t rows, int64_t cols, int64_t ld,
                  const void* col_scales, int col_dtype, int format, int group, const dq_outputs* out, void* workspace,
                  size_t workspace_bytes, void* stream);

@@ -53,7 +53,7 @@ def norm(lib, X=FAKE, r=None, xdt=1, rows=2, cols=64, g=FAKE, eps=1e-5, b=FAKE, 
     (dict(X=FAKE + 8), 1), (dict(g=FAKE + 2), 1), (dict(b=FAKE + 1), 1), (dict(r=FAKE), 1), (dict(ro=FAKE), 1),
     (dict(r=FAKE, ro=FAKE + 4), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
     (dict(out=outs(codes=FAKE + 4)), 1), (dict(out=outs(scales=None)), 1),
-    (dict(fmt=2, group=16, out=outs(sT=None)), 1), (dict(ws=None), 1), (dict(ws=FAKE + 128), 1), (dict(nbytes=255), 3),
+    (dict(fmt=2, group=16, out=outs(sT=None)), 1), (dict(fmt=2, group=16, ws=None), 1), (dict(ws=FAKE + 128), 1), (dict(nbytes=255), 3),
     (dict(fmt=2, group=16, nbytes=256), 3), (dict(rows=2 ** 40), 2),
 ])
 def test_norm_refusals(lib, kw, status):
