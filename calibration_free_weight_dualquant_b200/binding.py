@@ -371,19 +371,19 @@ def _call(device: torch.device, stream, f, *args):
             return f(stream.cuda_stream, *args)
 
 
-def _quantized(t: dict, f: Format, device, where: str) -> tuple:
+def _quantized(t: dict, f, device, where: str) -> tuple:
     """(rows, cols, struct) of a quantized matrix {"codes", "block_scales", "tensor_scale"}; DQError unless its
     tensors are the format's, on `device`."""
     codes, scales = t["codes"], t["block_scales"]
-    if codes.dim() != 2 or codes.dtype is not torch.uint8 or not codes.is_contiguous() or codes.device != device:
+    shape = codes.shape
+    if len(shape) != 2 or codes.dtype is not torch.uint8 or not codes.is_contiguous() or codes.device != device:
         raise DQError(1, where + ": codes must be a contiguous 2-D uint8 tensor on the call's device")
-    r, c = codes.shape
-    if f is not Format.MXFP8:
-        c *= 2
+    r, c = shape
+    c *= f.per_byte
     if (scales.dtype is not torch.uint8 or not scales.is_contiguous() or scales.device != device
-            or scales.shape != (r, c // DEFAULT_GROUP[f])):
+            or scales.shape != (r, c // f.group)):
         raise DQError(1, where + ": block_scales must be contiguous uint8 [rows][cols/group] on the call's device")
-    if f is not Format.NVFP4:
+    if not f.tensor_scale:
         return r, c, _Outputs(codes.data_ptr(), scales.data_ptr())
     s = t.get("tensor_scale")
     if s is None or s.dtype is not torch.float32 or s.numel() != 1 or s.device != device:
@@ -391,16 +391,26 @@ def _quantized(t: dict, f: Format, device, where: str) -> tuple:
     return r, c, _Outputs(codes.data_ptr(), scales.data_ptr(), s.data_ptr())
 
 
-_PRODUCT_FORMATS = {k: f for f in (Format.NVFP4, Format.MXFP4, Format.MXFP8) for k in (f, int(f), f.name.lower())}
+class _Spec:
+    """What a call needs of a format, as plain attributes (an IntEnum's hash and comparison cost a call each)."""
+    __slots__ = ("id", "group", "per_byte", "tensor_scale")
+
+    def __init__(self, f: Format):
+        self.id, self.group = int(f), DEFAULT_GROUP[f]
+        self.per_byte = 1 if f == Format.MXFP8 else 2
+        self.tensor_scale = f == Format.NVFP4
 
 
-def _product_format(fmt, group: Optional[int], where: str) -> Format:
+_PRODUCT_FORMATS = {k: _Spec(f) for f in (Format.NVFP4, Format.MXFP4, Format.MXFP8) for k in (f, int(f), f.name.lower())}
+
+
+def _product_format(fmt, group: Optional[int], where: str) -> _Spec:
     f = _PRODUCT_FORMATS.get(fmt)
     if f is None:
         _fmt(fmt)  # an unknown name is an error of its own
         raise DQError(2, where + ": nvfp4, mxfp4 and mxfp8 only")
-    if group is not None and group != DEFAULT_GROUP[f]:
-        raise DQError(2, where + ": group %d" % DEFAULT_GROUP[f])
+    if group is not None and group != f.group:
+        raise DQError(2, where + ": group %d" % f.group)
     return f
 
 
@@ -452,7 +462,7 @@ def _matmul(sp, codes, X, W, f, out, out_dtype, workspace, check):
     elif out.dtype not in _DTYPES or out.shape != (tokens, rows) or not out.is_contiguous() or out.device != dev:
         raise DQError(1, "dq_matmul: out must be contiguous f32/bf16/f16 [tokens, rows] on the call's device")
     wp, wn = _workspace(workspace, codes, MATMUL_WORKSPACE_BYTES if check else 0, "dq_matmul")
-    st = _lib.dq_matmul(xs, tokens, ws, rows, cols, f, DEFAULT_GROUP[f], out.data_ptr(), _DTYPES[out.dtype],
+    st = _lib.dq_matmul(xs, tokens, ws, rows, cols, f.id, f.group, out.data_ptr(), _DTYPES[out.dtype],
                         None if wp is None else wp.data_ptr(), wn, sp)
     if st != 0:
         raise DQError(st, "dq_matmul")
@@ -461,18 +471,18 @@ def _matmul(sp, codes, X, W, f, out, out_dtype, workspace, check):
     return out
 
 
-def _row_outputs(out: Optional[dict], like: torch.Tensor, rows: int, cols: int, f: Format, where: str) -> tuple:
+def _row_outputs(out: Optional[dict], like: torch.Tensor, rows: int, cols: int, f: _Spec, where: str) -> tuple:
     """(the output dict, its struct)."""
     if out is not None:
         r, c, struct = _quantized(out, f, like.device, where)
         if r != rows or c != cols:
             raise DQError(1, where + " must be [%d][%d columns]" % (rows, cols))
         return out, struct
-    if cols % DEFAULT_GROUP[f] != 0:
+    if cols % f.group != 0:
         raise DQError(1, where + ": %d columns are not a multiple of the group" % cols)
-    codes = like.new_empty((rows, cols if f is Format.MXFP8 else cols // 2), dtype=torch.uint8)
-    scales = codes.new_empty((rows, cols // DEFAULT_GROUP[f]))
-    if f is not Format.NVFP4:
+    codes = like.new_empty((rows, cols // f.per_byte), dtype=torch.uint8)
+    scales = codes.new_empty((rows, cols // f.group))
+    if not f.tensor_scale:
         return {"codes": codes, "block_scales": scales}, _Outputs(codes.data_ptr(), scales.data_ptr())
     s = like.new_empty(1, dtype=torch.float32)
     return ({"codes": codes, "block_scales": scales, "tensor_scale": s},
@@ -518,10 +528,10 @@ def _norm_quant(sp, X, weight, col_scales, f, residual, eps, out, residual_out, 
     out, struct = _row_outputs(out, X, rows, cols, f, "dq_norm_quant: out")
     if residual is not None and residual_out is None:
         residual_out = X.new_empty((rows, cols))
-    need = ACT_WORKSPACE_BYTES + 8 * rows if f is Format.NVFP4 else (ACT_WORKSPACE_BYTES if check else 0)
+    need = ACT_WORKSPACE_BYTES + 8 * rows if f.tensor_scale else (ACT_WORKSPACE_BYTES if check else 0)
     workspace, wn = _workspace(workspace, out["codes"], need, "dq_norm_quant")
     st = _lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), _DTYPES[X.dtype], rows, cols,
-                            gp, eps, bp, 1 if col_scales is None else _DTYPES[col_scales.dtype], f, DEFAULT_GROUP[f],
+                            gp, eps, bp, 1 if col_scales is None else _DTYPES[col_scales.dtype], f.id, f.group,
                             struct, None if residual is None else residual_out.data_ptr(),
                             None if workspace is None else workspace.data_ptr(), wn, sp)
     if st != 0:
@@ -565,10 +575,10 @@ def _glu_quant(sp, gate, up, one, col_scales, f, out, workspace, check):
     bp = None if col_scales is None else _channel_vector(col_scales, cols, _HALVES, gate.device,
                                                          "dq_glu_quant: col_scales")
     out, struct = _row_outputs(out, gate, rows, cols, f, "dq_glu_quant: out")
-    workspace, wn = _workspace(workspace, out["codes"], ACT_WORKSPACE_BYTES if check or f is Format.NVFP4 else 0,
+    workspace, wn = _workspace(workspace, out["codes"], ACT_WORKSPACE_BYTES if check or f.tensor_scale else 0,
                                "dq_glu_quant")
     st = _lib.dq_glu_quant(gp, upp, _DTYPES[gate.dtype], rows, cols, ld, bp,
-                           1 if col_scales is None else _DTYPES[col_scales.dtype], f, DEFAULT_GROUP[f], struct,
+                           1 if col_scales is None else _DTYPES[col_scales.dtype], f.id, f.group, struct,
                            None if workspace is None else workspace.data_ptr(), wn, sp)
     if st != 0:
         raise DQError(st, "dq_glu_quant")
