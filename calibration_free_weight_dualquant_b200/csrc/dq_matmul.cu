@@ -533,11 +533,13 @@ struct PairGeo {
 };
 
 struct PairLaunch {
-  unsigned tiles_m, tiles_n, tiles;  // products of 2^31 at most
+  unsigned tiles_m, tiles_n;  // their product is below 2^31
+  unsigned first, end;        // the tiles of this launch
   int unit_x, unit_w;
   int wide;   // rows of Y start at multiples of 32 bytes
   int vec4;   // fours of outputs are aligned
   int split;  // pairs of a cluster, each with its share of the K tiles of one tile
+  int last;   // no launch over the rest of the tiles follows
 };
 constexpr int kPartPitch = 260;  // floats of a partial tile's row in shared memory: conflict-free both ways
 
@@ -585,7 +587,7 @@ __device__ __forceinline__ void store_turned(const MatmulProblem& p, float* turn
 template <bool OUT32>
 static __device__ __noinline__ void pair_give_up(const MatmulProblem& p, const PairLaunch& l, unsigned i, unsigned pairs,
                                                  int rank, int warp) {
-  for (; i < l.tiles; i += pairs) {
+  for (; i < l.end; i += pairs) {
     int64_t m, n;
     pair_tile(l, i, m, n);
     const int64_t t = m * 256 + rank * 128 + 32 * (warp & 3) + (threadIdx.x & 31), n0 = n * 256 + 128 * (warp >> 2);
@@ -632,9 +634,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  griddep_launch_dependents();
-  griddep_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
+  // The first launch's whole waves run before the rest's; what the call reads is
+  // complete when the first launch's wait returns, and only then may the second
+  // begin, which waits for the first at its end.
+  if (l.last) griddep_launch_dependents();
+  if (l.first == 0) griddep_wait();
+  if (!l.last) griddep_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0 && flags && l.first == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   MmSlot at;
   bool gave_up = false;
 
@@ -642,7 +648,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (elect_one()) {
       bool ok = true;
       int64_t issued = 0;
-      for (unsigned i = pair; i < l.tiles && ok; i += pairs) {
+      for (unsigned i = l.first + pair; i < l.end && ok; i += pairs) {
         int64_t m, n;
         pair_tile(l, i, m, n);
         for (int kt = k0; kt < k1; ++kt, ++issued) {
@@ -662,7 +668,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (rank == 0 && elect_one()) {
       unsigned turn = 0, set = 0, piece = 0;
       bool ok = true;
-      for (unsigned i = pair; i < l.tiles && ok; i += pairs, turn ^= 1) {
+      for (unsigned i = l.first + pair; i < l.end && ok; i += pairs, turn ^= 1) {
         if (!(ok = mm_wait(&acc_empty, turn ^ 1, flags))) break;
         tc_fence_after();
         for (int kt = k0; kt < k1; ++kt, set ^= 1) {
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const bool of_x = block == 0;
     ScaleTurn t{warp & 1};
     bool ok = true;
-    for (unsigned i = pair; i < l.tiles && ok; i += pairs) {
+    for (unsigned i = l.first + pair; i < l.end && ok; i += pairs) {
       int64_t m, n;
       pair_tile(l, i, m, n);
       ok = scale_warp<true>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int q = warp & 3, half = warp >> 2;
     float* turned = reinterpret_cast<float*>(scales + 2 * G::kScales) + warp * 32 * 33;
     unsigned turn = 0;
-    for (unsigned i = pair; i < l.tiles; i += pairs, turn ^= 1) {
+    for (unsigned i = l.first + pair; i < l.end; i += pairs, turn ^= 1) {
       int64_t m, n;
       pair_tile(l, i, m, n);
       if (!__all_sync(0xffffffffu, mm_wait(&acc_full, turn, flags))) {
@@ -808,13 +814,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     float f1, f2_;
     tensor_factors(p, f1, f2_);
     int64_t m, n;
-    pair_tile(l, pair, m, n);
-    const int rows = 128 / l.split;
+    pair_tile(l, l.first + pair, m, n);
+    const int rows = (128 + l.split - 1) / l.split;
     const uint32_t part = smem_u32(ring);
     for (int e = threadIdx.x; e < rows * 64; e += kPairThreads) {
       const int row = share * rows + (e >> 6), col = 4 * (e & 63);
       const int64_t t = m * 256 + rank * 128 + row, nn = n * 256 + col;
-      if (t >= p.T || nn >= p.N) continue;
+      if (row >= 128 || t >= p.T || nn >= p.N) continue;
       float4 v[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -827,6 +833,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       y_store4(p.y, p.y_dt, t * p.N + nn, o, p.N - nn, l.vec4);
     }
   }
+  if (l.first != 0) griddep_wait();
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still signal it or read its shared memory
   if (warp == 9) {
@@ -877,7 +884,9 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
   MmLaunch l;
   l.split = 1;
-  while (l.split < 8 && l.split < nk && tiles * (l.split + 1) <= sms) ++l.split;
+  // clusters of more than 2 CTAs leave some SMs of a GPC unused: 132 of 148 SMs can hold clusters of 4 or 6, 120 of 8
+  while (l.split < 8 && l.split < nk && tiles * (l.split + 1) <= (l.split < 2 ? sms : (l.split < 6 ? sms * 8 / 9 : sms * 4 / 5)))
+    ++l.split;
   const int64_t per = (nk + l.split - 1) / l.split;
   // one CTA an SM takes all shared memory, more tiles share an SM by three
   const int room = ((tiles * l.split <= sms ? 220 : 74) * 1024 - 2 * G::kScales - 1024) / G::kStage;
@@ -907,8 +916,12 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   return launch_early(kern, (unsigned)(tiles * l.split), kMmThreads, (size_t)smem, l.split, st, p, l, wmap, xmap);
 }
 
+// Whole waves of pairs first; the tiles left over, or all of them where they do
+// not fill a wave, split their columns over the pairs of a cluster, if clusters
+// that large have room for them at once.  (1500 x 4096 x 14336 MXFP4, 96 tiles on
+// 74 pairs: 42 us as two waves.)
 template <int FMT, bool OUT32>
-static cudaError_t matmul_pair(const MatmulProblem& p, int split, int sms, cudaStream_t st) {
+static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st) {
   using G = PairGeo<FMT>;
   CUtensorMap wmap, xmap;
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
@@ -917,17 +930,40 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int split, int sms, cudaS
   PairLaunch l;
   l.tiles_m = (unsigned)((p.T + 255) / 256);
   l.tiles_n = (unsigned)((p.N + 255) / 256);
-  l.tiles = l.tiles_m * l.tiles_n;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
   l.wide = ((uintptr_t)p.y | (uintptr_t)(p.N * (OUT32 ? 4 : 2))) % 32 == 0;
+  l.vec4 = vec4_rows(p);
   auto kern = k_matmul_pair<FMT, OUT32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (e != cudaSuccess) return e;
-  l.vec4 = vec4_rows(p);
+  const unsigned tiles = l.tiles_m * l.tiles_n, pairs = (unsigned)sms / 2;
+  const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
+  const unsigned rest = tiles % pairs;
+  int split = 1;
+  for (int s = 4; s > 1 && split == 1 && rest > 0; --s) {
+    if (nk < 4 * s || rest * s > pairs) continue;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at;
+    cluster_config(&cfg, &at, rest * 2 * s, kPairThreads, (size_t)G::kSmem, 2 * s);
+    int room = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&room, kern, &cfg)) != cudaSuccess) return e;
+    if ((unsigned)room >= rest) split = s;
+  }
+  const unsigned whole = split > 1 ? tiles - rest : tiles;
+  if (whole > 0) {
+    l.first = 0;
+    l.end = whole;
+    l.split = 1;
+    l.last = whole == tiles;
+    e = launch_early(kern, 2 * (whole < pairs ? whole : pairs), kPairThreads, (size_t)G::kSmem, 2, st, p, l, wmap, xmap);
+    if (e != cudaSuccess || l.last) return e;
+  }
+  l.first = whole;
+  l.end = tiles;
   l.split = split;
-  const unsigned pairs = split > 1 ? l.tiles * split : (l.tiles < (unsigned)sms / 2 ? l.tiles : (unsigned)sms / 2);
-  return launch_early(kern, 2 * pairs, kPairThreads, (size_t)G::kSmem, 2 * split, st, p, l, wmap, xmap);
+  l.last = 1;
+  return launch_early(kern, rest * 2 * split, kPairThreads, (size_t)G::kSmem, 2 * split, st, p, l, wmap, xmap);
 }
 
 template <int FMT>
@@ -937,10 +973,7 @@ static cudaError_t matmul_fmt(const MatmulProblem& p, int sms, cudaStream_t st) 
   if (p.T <= 16) return matmul_tc<FMT, 16>(p, sms, st);
   if (p.T <= 32) return matmul_tc<FMT, 32>(p, sms, st);
   if (p.T <= 64) return matmul_tc<FMT, 64>(p, sms, st);
-  const int64_t tiles = (p.N + 255) / 256 * ((p.T + 255) / 256);
-  const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
-  const int split = tiles * 4 <= sms / 4 && nk >= 8 ? 4 : (tiles * 2 <= sms / 2 && nk >= 8 ? 2 : 1);
-  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, split, sms, st) : matmul_pair<FMT, false>(p, split, sms, st);
+  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, sms, st) : matmul_pair<FMT, false>(p, sms, st);
 }
 
 }  // namespace dq

@@ -55,6 +55,8 @@ SHAPES = [
     (16, 4096, 14336), (17, 255, 288), (31, 128, 1024), (33, 257, 1056), (64, 640, 2048), (65, 64, 320),
     (100, 1001, 1056), (128, 128, 128), (129, 1024, 4096), (255, 384, 544), (256, 256, 256), (257, 513, 1120),
     (300, 96, 8192), (700, 1000, 1312), (1025, 2049, 160),
+    # tiles of 256 x 256 left over after whole waves of the SM pairs, split in 2, 3 and 4, and a part of a wave
+    (2300, 2500, 4096), (2500, 2300, 1024), (2000, 2600, 4096), (500, 2049, 4096), (300, 600, 4096),
 ]
 
 
