@@ -386,6 +386,10 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
+  if (warp == 0 && elect_one()) {
+    tma_prefetch_map(&wmap);
+    tma_prefetch_map(&xmap);
+  }
   if (l.early) griddep_launch_dependents();
   griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
@@ -536,7 +540,7 @@ struct PairLaunch {
   unsigned tiles_m, tiles_n;  // their product is below 2^31
   unsigned first, end;        // the tiles of this launch
   int unit_x, unit_w;
-  int wide;   // rows of Y start at multiples of 32 bytes
+  int rows16;  // rows of Y start at multiples of 16 bytes
   int vec4;   // fours of outputs are aligned
   int split;  // pairs of a cluster, each with its share of the K tiles of one tile
   int last;   // no launch over the rest of the tiles follows
@@ -552,34 +556,54 @@ __device__ __forceinline__ void pair_tile(const PairLaunch& l, unsigned i, int64
   n = col;
 }
 
-__device__ __forceinline__ void st_global_32b(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// Stores 32 rows x 32 columns of a warp, lane = row, v[c] = column c (16-bit
-// outputs: two columns a word), where rows of Y have no useful alignment:
-// through the warp's padded block of shared memory, so that lanes write
-// neighbouring columns.
+// Stores 32 rows x 128 bytes of a warp from (row t, column n) on, lane = row, v =
+// its 32 words (16-bit outputs: two columns a word), through the warp's block of
+// shared memory, so that lanes write neighbouring columns.  Rows of Y that start
+// at multiples of 16 bytes: 16-byte chunks of a row at places that depend on the
+// row (conflict-free both ways), whole 128-byte lines of 4 rows an instruction.
+// Others: 32 columns at a time in a padded block, an output a lane.  (An aligned
+// word a lane, shifted into place, took longer: 15.9 us against 13.2 for 1000 x
+// 1001 x 1056 NVFP4.)
 template <bool OUT32>
-__device__ __forceinline__ void store_turned(const MatmulProblem& p, float* turn, const uint32_t* v, int64_t t, int64_t n) {
+__device__ __forceinline__ void store_rows(const MatmulProblem& p, uint4* stage, const uint32_t* v, int64_t t, int64_t n,
+                                           bool rows16) {
+  constexpr int ES = OUT32 ? 4 : 2, COLS = 128 / ES;
   const int lane = threadIdx.x & 31;
-  uint32_t* b = reinterpret_cast<uint32_t*>(turn);
-  __syncwarp();
+  const int rows = (int)max((int64_t)0, min((int64_t)32, p.T - t)), cols = (int)max((int64_t)0, min((int64_t)COLS, p.N - n));
+  unsigned char* y = reinterpret_cast<unsigned char*>(p.y) + (t * p.N + n) * ES;
+  const int64_t pitch = p.N * ES;
+  if (rows16) {  // the row's end is a multiple of 16 bytes too
+    __syncwarp();
 #pragma unroll
-  for (int c = 0; c < 32; ++c)
-    b[lane * 33 + c] = OUT32 ? v[c] : ((c & 1) ? v[c / 2] >> 16 : v[c / 2] & 0xFFFFu);
-  __syncwarp();
-  const int rows = (int)max((int64_t)0, min((int64_t)32, p.T - t));
-  if (n + lane < p.N)
-    for (int r = 0; r < rows; ++r) {
-      const int64_t at = (t + r) * p.N + n + lane;
-      if (OUT32)
-        reinterpret_cast<uint32_t*>(p.y)[at] = b[r * 33 + lane];
-      else
-        reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)b[r * 33 + lane];
+    for (int c = 0; c < 8; ++c)
+      stage[lane * 8 + (c ^ (lane & 7))] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    __syncwarp();
+    const int c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (r < rows && c * 16 < cols * ES)
+        *reinterpret_cast<uint4*>(y + r * pitch + c * 16) = stage[r * 8 + (c ^ (r & 7))];
     }
+  } else {
+    uint32_t* b = reinterpret_cast<uint32_t*>(stage);
+#pragma unroll
+    for (int k = 0; k < COLS / 32; ++k) {
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        b[lane * 33 + c] = OUT32 ? v[c] : ((c & 1) ? v[16 * k + c / 2] >> 16 : v[16 * k + c / 2] & 0xFFFFu);
+      __syncwarp();
+      const int c = 32 * k + lane;
+      if (c < cols)
+        for (int r = 0; r < rows; ++r) {
+          if (OUT32)
+            *reinterpret_cast<uint32_t*>(y + r * pitch + c * 4) = b[r * 33 + lane];
+          else
+            *reinterpret_cast<uint16_t*>(y + r * pitch + c * 2) = (uint16_t)b[r * 33 + lane];
+        }
+    }
+  }
 }
 
 // A wait ran out: this warp's part of the tiles i, i + pairs, ... becomes NaN, so
@@ -637,6 +661,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   // The first launch's whole waves run before the rest's; what the call reads is
   // complete when the first launch's wait returns, and only then may the second
   // begin, which waits for the first at its end.
+  if (warp == 8 && elect_one()) {
+    tma_prefetch_map(&xmap);
+    tma_prefetch_map(&wmap);
+  }
   if (l.last) griddep_launch_dependents();
   if (l.first == 0) griddep_wait();
   if (!l.last) griddep_launch_dependents();
@@ -715,7 +743,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     float f1, f2_;
     tensor_factors(p, f1, f2_);
     const int q = warp & 3, half = warp >> 2;
-    float* turned = reinterpret_cast<float*>(scales + 2 * G::kScales) + warp * 32 * 33;
+    uint4* stage = reinterpret_cast<uint4*>(scales + 2 * G::kScales) + warp * (32 * 33 / 4);
     unsigned turn = 0;
     for (unsigned i = l.first + pair; i < l.end; i += pairs, turn ^= 1) {
       int64_t m, n;
@@ -729,7 +757,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       tc_fence_after();
       const uint32_t src = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
-      const int64_t t0 = m * 256 + rank * 128 + 32 * q, t = t0 + lane, nn = n * 256 + 128 * half;
+      const int64_t t0 = m * 256 + rank * 128 + 32 * q, nn = n * 256 + 128 * half;
       if (l.split > 1) {  // the partial tile to the idle ring, joined below
         float* part = reinterpret_cast<float*>(ring) + (32 * q + lane) * kPartPitch + 128 * half;
 #pragma unroll 1
@@ -755,29 +783,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(&acc_empty, leader);
           }
-          if (FMT == FMT_NVFP4) {
-            const f2 f = splat(f1);
+          if (FMT == FMT_NVFP4 && f2_ != 1.f) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              f2 y = mul2(pk(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), f);
-              if (f2_ != 1.f) y = mul2(y, splat(f2_));
-              o[32 * c + e] = pack16(lo_of(y), hi_of(y), p.y_dt);
-            }
-          } else {
+            for (int e = 0; e < 64; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f2_);
+          }
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[32 * c + e] = pack16(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), p.y_dt);
+          for (int e = 0; e < 32; ++e) {
+            float a = __uint_as_float(v[2 * e]), b = __uint_as_float(v[2 * e + 1]);
+            if (FMT == FMT_NVFP4) a *= f1, b *= f1;
+            o[32 * c + e] = pack16(a, b, p.y_dt);
           }
         }
-        if (l.wide) {
-          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + t * p.N + nn;
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (t < p.T && nn + 16 * c < p.N) st_global_32b(y + 16 * c, o + 8 * c);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) store_turned<false>(p, turned, o + 16 * c, t0, nn + 32 * c);
-        }
+        for (int c = 0; c < 2; ++c) store_rows<false>(p, stage, o + 32 * c, t0, nn + 64 * c, l.rows16);
       } else {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -791,14 +809,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f1 * f2_);
-          if (l.wide) {
-            uint32_t* y = reinterpret_cast<uint32_t*>(p.y) + t * p.N + nn + 32 * c;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (t < p.T && nn + 32 * c + 8 * e < p.N) st_global_32b(y + 8 * e, v + 8 * e);
-          } else {
-            store_turned<true>(p, turned, v, t0, nn + 32 * c);
-          }
+          store_rows<true>(p, stage, v, t0, nn + 32 * c, l.rows16);
         }
       }
     }
@@ -918,8 +929,9 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
 
 // Whole waves of pairs first; the tiles left over, or all of them where they do
 // not fill a wave, split their columns over the pairs of a cluster, if clusters
-// that large have room for them at once.  (1500 x 4096 x 14336 MXFP4, 96 tiles on
-// 74 pairs: 42 us as two waves.)
+// that large have room for them at once and the wave saved is long enough.
+// (1500 x 4096 x 14336 MXFP8, 96 tiles on 74 pairs: 82 us as two waves, 72 so;
+// 2048 x 14336 x 4096 NVFP4, 448 tiles: 62 us as seven waves, 66 so.)
 template <int FMT, bool OUT32>
 static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st) {
   using G = PairGeo<FMT>;
@@ -932,7 +944,7 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
   l.tiles_n = (unsigned)((p.N + 255) / 256);
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
-  l.wide = ((uintptr_t)p.y | (uintptr_t)(p.N * (OUT32 ? 4 : 2))) % 32 == 0;
+  l.rows16 = ((uintptr_t)p.y | (uintptr_t)(p.N * (OUT32 ? 4 : 2))) % 16 == 0;
   l.vec4 = vec4_rows(p);
   auto kern = k_matmul_pair<FMT, OUT32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
@@ -942,7 +954,8 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
   const unsigned rest = tiles % pairs;
   int split = 1;
   for (int s = 4; s > 1 && split == 1 && rest > 0; --s) {
-    if (nk < 4 * s || rest * s > pairs) continue;
+    // K tiles saved, about 0.3 us each, against the joining of the partial tiles (4 us) and a launch of its own (4 us)
+    if (rest * s > pairs || nk * (s - 1) < (tiles > rest ? 28 : 12) * s) continue;
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute at;
     cluster_config(&cfg, &at, rest * 2 * s, kPairThreads, (size_t)G::kSmem, 2 * s);

@@ -121,6 +121,11 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t leader = 0) {
                  : "memory");
 }
 
+// Brings a tensor map (a kernel parameter) close before its first copy.
+__device__ __forceinline__ void tma_prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // Tensor copy of a pair's CTA into its own shared memory, completing on the
 // even CTA's barrier (the rank is bit 24 of a shared address in a cluster).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int x, int y, uint64_t* bar) {
