@@ -489,6 +489,11 @@ def _row_outputs(out: Optional[dict], like: torch.Tensor, rows: int, cols: int, 
             _Outputs(codes.data_ptr(), scales.data_ptr(), s.data_ptr()))
 
 
+def _check_like(t: torch.Tensor, X: torch.Tensor, where: str):
+    if t.dtype is not X.dtype or t.shape != X.shape or not t.is_contiguous() or t.device != X.device:
+        raise DQError(1, where + " must match X")
+
+
 def _channel_vector(t: torch.Tensor, cols: int, dtypes, device, where: str) -> int:
     if t.dtype not in dtypes or t.numel() != cols or not t.is_contiguous() or t.device != device:
         raise DQError(1, where + " must be a contiguous 16-bit float [cols] tensor on the call's device")
@@ -496,6 +501,7 @@ def _channel_vector(t: torch.Tensor, cols: int, dtypes, device, where: str) -> i
 
 
 _HALVES = (torch.bfloat16, torch.float16)
+_HALF_DTYPES = {t: _DTYPES[t] for t in _HALVES}
 
 
 def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: Optional[torch.Tensor], fmt,
@@ -508,18 +514,20 @@ def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: O
     gets NaN scales; ``check`` waits and raises on it, and a ``workspace`` reports it later without that."""
     load_library()
     f = _product_format(fmt, group, "dq_norm_quant")
-    if not X.is_cuda or X.dtype not in _HALVES or not X.is_contiguous() or X.dim() != 2:
+    xdt = _HALF_DTYPES.get(X.dtype)
+    if xdt is None or not X.is_cuda or not X.is_contiguous() or X.dim() != 2:
         raise DQError(1, "dq_norm_quant: X must be a contiguous 2-D bf16/f16 CUDA tensor")
-    for t, name in ((residual, "residual"), (residual_out, "residual_out")):
-        if t is not None and (t.dtype != X.dtype or t.shape != X.shape or not t.is_contiguous() or t.device != X.device):
-            raise DQError(1, "dq_norm_quant: %s must match X" % name)
-    if residual is None and residual_out is not None:
+    if residual is not None:
+        _check_like(residual, X, "dq_norm_quant: residual")
+        if residual_out is not None:
+            _check_like(residual_out, X, "dq_norm_quant: residual_out")
+    elif residual_out is not None:
         raise DQError(1, "dq_norm_quant: residual_out without a residual")
-    return _call(X.device, stream, _norm_quant, X, weight, col_scales, f, residual, eps, out, residual_out, workspace,
+    return _call(X.device, stream, _norm_quant, X, xdt, weight, col_scales, f, residual, eps, out, residual_out, workspace,
                  check)
 
 
-def _norm_quant(sp, X, weight, col_scales, f, residual, eps, out, residual_out, workspace, check):
+def _norm_quant(sp, X, xdt, weight, col_scales, f, residual, eps, out, residual_out, workspace, check):
     rows, cols = X.shape
     dev = X.device
     gp = None if weight is None else _channel_vector(weight, cols, (X.dtype,), dev,
@@ -530,9 +538,8 @@ def _norm_quant(sp, X, weight, col_scales, f, residual, eps, out, residual_out, 
         residual_out = X.new_empty((rows, cols))
     need = ACT_WORKSPACE_BYTES + 8 * rows if f.tensor_scale else (ACT_WORKSPACE_BYTES if check else 0)
     workspace, wn = _workspace(workspace, out["codes"], need, "dq_norm_quant")
-    st = _lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), _DTYPES[X.dtype], rows, cols,
-                            gp, eps, bp, 1 if col_scales is None else _DTYPES[col_scales.dtype], f.id, f.group,
-                            struct, None if residual is None else residual_out.data_ptr(),
+    st = _lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), xdt, rows, cols, gp, eps,
+                            bp, 1 if col_scales is None else _HALF_DTYPES[col_scales.dtype], f.id, f.group, struct, None if residual is None else residual_out.data_ptr(),
                             None if workspace is None else workspace.data_ptr(), wn, sp)
     if st != 0:
         raise DQError(st, "dq_norm_quant")
