@@ -1,14 +1,16 @@
-"""Thin ctypes binding of ``libdq.so`` (C ABI in ``include/dq.h``).
+"""Thin binding of ``libdq.so`` (C ABI in ``include/dq.h``).
 
-Argument marshalling only: torch supplies device memory and the current
-stream; every step of the solver runs in the library's CUDA kernels.  There is
-no CPU fallback -- without the built library or a CUDA device every call
-raises :class:`DQError`.
+Argument marshalling only, by ctypes, or for the linear layer's short calls by
+the compiled module of ``csrc/dq_torch.cpp``: torch supplies device memory and
+the current stream; every step runs in the library's CUDA kernels.  There is no
+CPU fallback -- without the built libraries or a CUDA device every call raises
+:class:`DQError`.
 """
 from __future__ import annotations
 
 import ctypes
 import enum
+import importlib.util
 import os
 from typing import Optional
 
@@ -16,6 +18,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libdq.so")
+MARSHAL_PATH = os.path.join(_PKG, "lib", "_dq_torch.so")
 
 STATUS = {0: "DQ_OK", 1: "DQ_EINVAL", 2: "DQ_EUNSUPPORTED", 3: "DQ_EWORKSPACE", 4: "DQ_ENONFINITE", 5: "DQ_ECUDA"}
 
@@ -121,6 +124,25 @@ def load_library():
     lib.dq_status_str.restype = ctypes.c_char_p
     _lib = lib
     return lib
+
+
+_marshal = None
+
+
+def load_marshal():
+    """Load the compiled marshalling of the linear layer's calls (built in-tree by ``build.py``); raise if it is
+    missing."""
+    global _marshal
+    if _marshal is None:
+        load_library()
+        if not os.path.exists(MARSHAL_PATH):
+            raise DQError(5, "load_marshal: %s is not built (run __graft_entry__.build())" % MARSHAL_PATH)
+        spec = importlib.util.spec_from_file_location("_dq_torch", MARSHAL_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_error(DQError)
+        _marshal = m
+    return _marshal
 
 
 def _fmt(fmt) -> Format:
@@ -371,62 +393,18 @@ def _call(device: torch.device, stream, f, *args):
             return f(stream.cuda_stream, *args)
 
 
-def _quantized(t: dict, f, device, where: str) -> tuple:
-    """(rows, cols, struct) of a quantized matrix {"codes", "block_scales", "tensor_scale"}; DQError unless its
-    tensors are the format's, on `device`."""
-    codes, scales = t["codes"], t["block_scales"]
-    shape = codes.shape
-    if len(shape) != 2 or codes.dtype is not torch.uint8 or not codes.is_contiguous() or codes.device != device:
-        raise DQError(1, where + ": codes must be a contiguous 2-D uint8 tensor on the call's device")
-    r, c = shape
-    c *= f.per_byte
-    if (scales.dtype is not torch.uint8 or not scales.is_contiguous() or scales.device != device
-            or scales.shape != (r, c // f.group)):
-        raise DQError(1, where + ": block_scales must be contiguous uint8 [rows][cols/group] on the call's device")
-    if not f.tensor_scale:
-        return r, c, _Outputs(codes.data_ptr(), scales.data_ptr())
-    s = t.get("tensor_scale")
-    if s is None or s.dtype is not torch.float32 or s.numel() != 1 or s.device != device:
-        raise DQError(1, where + ": NVFP4 needs a one-element float32 tensor_scale on the call's device")
-    return r, c, _Outputs(codes.data_ptr(), scales.data_ptr(), s.data_ptr())
+_PRODUCT_FORMATS = {k: (int(f), DEFAULT_GROUP[f]) for f in (Format.NVFP4, Format.MXFP4, Format.MXFP8)
+                    for k in (f, int(f), f.name.lower())}
 
 
-class _Spec:
-    """What a call needs of a format, as plain attributes (an IntEnum's hash and comparison cost a call each)."""
-    __slots__ = ("id", "group", "per_byte", "tensor_scale")
-
-    def __init__(self, f: Format):
-        self.id, self.group = int(f), DEFAULT_GROUP[f]
-        self.per_byte = 1 if f == Format.MXFP8 else 2
-        self.tensor_scale = f == Format.NVFP4
-
-
-_PRODUCT_FORMATS = {k: _Spec(f) for f in (Format.NVFP4, Format.MXFP4, Format.MXFP8) for k in (f, int(f), f.name.lower())}
-
-
-def _product_format(fmt, group: Optional[int], where: str) -> _Spec:
+def _product_format(fmt, group: Optional[int], where: str) -> int:
     f = _PRODUCT_FORMATS.get(fmt)
     if f is None:
         _fmt(fmt)  # an unknown name is an error of its own
         raise DQError(2, where + ": nvfp4, mxfp4 and mxfp8 only")
-    if group is not None and group != f.group:
-        raise DQError(2, where + ": group %d" % f.group)
-    return f
-
-
-def _workspace(workspace: Optional[torch.Tensor], codes: torch.Tensor, nbytes: int, where: str) -> tuple:
-    """(the workspace tensor or None, its bytes): the caller's, or a new one of nbytes next to `codes`."""
-    if workspace is None:
-        return (codes.new_empty(nbytes), nbytes) if nbytes else (None, 0)
-    if workspace.device != codes.device or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
-        raise DQError(1, where + ": workspace must be a contiguous uint8 tensor on the call's device")
-    return workspace, workspace.numel()
-
-
-def _raise_device_status(workspace: torch.Tensor, stream_ptr: int, where: str):
-    st = _lib.dq_sync_status(workspace.data_ptr(), stream_ptr)
-    if st != 0:
-        raise DQError(st, where + " (device)")
+    if group is not None and group != f[1]:
+        raise DQError(2, where + ": group %d" % f[1])
+    return f[0]
 
 
 MATMUL_WORKSPACE_BYTES = 256
@@ -441,67 +419,15 @@ def dq_matmul(X: dict, W: dict, fmt, group: Optional[int] = None, out: Optional[
     dq_glu_quant and dq_solve return them, both in ``fmt`` (nvfp4, mxfp4 or mxfp8).  ``out`` (its dtype then
     counts, not ``out_dtype``) keeps the call free of allocations; ``check`` waits for the stream and raises on
     a device-reported status, which a ``workspace`` of MATMUL_WORKSPACE_BYTES reports later without it."""
-    load_library()
+    m = _marshal or load_marshal()
     f = _product_format(fmt, group, "dq_matmul")
     codes = X["codes"]
     if not codes.is_cuda:
         raise DQError(1, "dq_matmul: X must be on a CUDA device")
-    return _call(codes.device, stream, _matmul, codes, X, W, f, out, out_dtype, workspace, check)
-
-
-def _matmul(sp, codes, X, W, f, out, out_dtype, workspace, check):
-    dev = codes.device
-    tokens, cols, xs = _quantized(X, f, dev, "dq_matmul: X")
-    rows, wcols, ws = _quantized(W, f, dev, "dq_matmul: W")
-    if wcols != cols:
-        raise DQError(1, "dq_matmul: W has %d columns and X %d" % (wcols, cols))
-    if out is None:
-        if out_dtype not in _DTYPES:
-            raise DQError(1, "dq_matmul: out_dtype must be float32, bfloat16 or float16")
-        out = codes.new_empty((tokens, rows), dtype=out_dtype)
-    elif out.dtype not in _DTYPES or out.shape != (tokens, rows) or not out.is_contiguous() or out.device != dev:
-        raise DQError(1, "dq_matmul: out must be contiguous f32/bf16/f16 [tokens, rows] on the call's device")
-    wp, wn = _workspace(workspace, codes, MATMUL_WORKSPACE_BYTES if check else 0, "dq_matmul")
-    st = _lib.dq_matmul(xs, tokens, ws, rows, cols, f.id, f.group, out.data_ptr(), _DTYPES[out.dtype],
-                        None if wp is None else wp.data_ptr(), wn, sp)
-    if st != 0:
-        raise DQError(st, "dq_matmul")
-    if check:
-        _raise_device_status(wp, sp, "dq_matmul")
-    return out
-
-
-def _row_outputs(out: Optional[dict], like: torch.Tensor, rows: int, cols: int, f: _Spec, where: str) -> tuple:
-    """(the output dict, its struct)."""
-    if out is not None:
-        r, c, struct = _quantized(out, f, like.device, where)
-        if r != rows or c != cols:
-            raise DQError(1, where + " must be [%d][%d columns]" % (rows, cols))
-        return out, struct
-    if cols % f.group != 0:
-        raise DQError(1, where + ": %d columns are not a multiple of the group" % cols)
-    codes = like.new_empty((rows, cols // f.per_byte), dtype=torch.uint8)
-    scales = codes.new_empty((rows, cols // f.group))
-    if not f.tensor_scale:
-        return {"codes": codes, "block_scales": scales}, _Outputs(codes.data_ptr(), scales.data_ptr())
-    s = like.new_empty(1, dtype=torch.float32)
-    return ({"codes": codes, "block_scales": scales, "tensor_scale": s},
-            _Outputs(codes.data_ptr(), scales.data_ptr(), s.data_ptr()))
-
-
-def _check_like(t: torch.Tensor, X: torch.Tensor, where: str):
-    if t.dtype is not X.dtype or t.shape != X.shape or not t.is_contiguous() or t.device != X.device:
-        raise DQError(1, where + " must match X")
-
-
-def _channel_vector(t: torch.Tensor, cols: int, dtypes, device, where: str) -> int:
-    if t.dtype not in dtypes or t.numel() != cols or not t.is_contiguous() or t.device != device:
-        raise DQError(1, where + " must be a contiguous 16-bit float [cols] tensor on the call's device")
-    return t.data_ptr()
-
-
-_HALVES = (torch.bfloat16, torch.float16)
-_HALF_DTYPES = {t: _DTYPES[t] for t in _HALVES}
+    dt = _DTYPES.get(out_dtype)
+    if dt is None:
+        raise DQError(1, "dq_matmul: out_dtype must be float32, bfloat16 or float16")
+    return _call(codes.device, stream, m.matmul, X, W, f, out, dt, workspace, bool(check))
 
 
 def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: Optional[torch.Tensor], fmt,
@@ -512,44 +438,12 @@ def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: O
     scales, quantized row-wise in ``fmt`` (mxfp8, mxfp4 or nvfp4).  Returns the quantized matrix with
     out["residual"] = h (with a residual; ``residual_out`` may be X or the residual itself).  A non-finite row
     gets NaN scales; ``check`` waits and raises on it, and a ``workspace`` reports it later without that."""
-    load_library()
+    m = _marshal or load_marshal()
     f = _product_format(fmt, group, "dq_norm_quant")
-    xdt = _HALF_DTYPES.get(X.dtype)
-    if xdt is None or not X.is_cuda or not X.is_contiguous() or X.dim() != 2:
-        raise DQError(1, "dq_norm_quant: X must be a contiguous 2-D bf16/f16 CUDA tensor")
-    if residual is not None:
-        _check_like(residual, X, "dq_norm_quant: residual")
-        if residual_out is not None:
-            _check_like(residual_out, X, "dq_norm_quant: residual_out")
-    elif residual_out is not None:
-        raise DQError(1, "dq_norm_quant: residual_out without a residual")
-    return _call(X.device, stream, _norm_quant, X, xdt, weight, col_scales, f, residual, eps, out, residual_out, workspace,
-                 check)
-
-
-def _norm_quant(sp, X, xdt, weight, col_scales, f, residual, eps, out, residual_out, workspace, check):
-    rows, cols = X.shape
-    dev = X.device
-    gp = None if weight is None else _channel_vector(weight, cols, (X.dtype,), dev,
-                                                     "dq_norm_quant: weight (in X's dtype)")
-    bp = None if col_scales is None else _channel_vector(col_scales, cols, _HALVES, dev, "dq_norm_quant: col_scales")
-    out, struct = _row_outputs(out, X, rows, cols, f, "dq_norm_quant: out")
-    if residual is not None and residual_out is None:
-        residual_out = X.new_empty((rows, cols))
-    need = ACT_WORKSPACE_BYTES + 8 * rows if f.tensor_scale else (ACT_WORKSPACE_BYTES if check else 0)
-    workspace, wn = _workspace(workspace, out["codes"], need, "dq_norm_quant")
-    st = _lib.dq_norm_quant(X.data_ptr(), None if residual is None else residual.data_ptr(), xdt, rows, cols, gp, eps,
-                            bp, 1 if col_scales is None else _HALF_DTYPES[col_scales.dtype], f.id, f.group, struct, None if residual is None else residual_out.data_ptr(),
-                            None if workspace is None else workspace.data_ptr(), wn, sp)
-    if st != 0:
-        raise DQError(st, "dq_norm_quant")
-    if check:
-        _raise_device_status(workspace, sp, "dq_norm_quant")
-    if residual is not None:
-        out["residual"] = residual_out
-    if workspace is not None:
-        out["workspace"] = workspace
-    return out
+    if not X.is_cuda:
+        raise DQError(1, "dq_norm_quant: X must be on a CUDA device")
+    return _call(X.device, stream, m.norm_quant, X, weight, col_scales, f, residual, eps, out, residual_out, workspace,
+                 bool(check))
 
 
 def dq_glu_quant(X, col_scales: Optional[torch.Tensor], fmt, group: Optional[int] = None, out: Optional[dict] = None,
@@ -557,43 +451,12 @@ def dq_glu_quant(X, col_scales: Optional[torch.Tensor], fmt, group: Optional[int
     """Enqueue dq_glu_quant: silu(gate) * up times the column inverse scales, quantized row-wise in ``fmt``
     (mxfp8, mxfp4 or nvfp4).  X is one tensor [tokens, 2 cols], gate left of up (a product over stacked gate and
     up weights), or a pair (gate, up) of [tokens, cols] tensors with one row stride."""
-    load_library()
+    m = _marshal or load_marshal()
     f = _product_format(fmt, group, "dq_glu_quant")
-    one = isinstance(X, torch.Tensor)
-    gate, up = (X, X) if one else X
-    for t in (gate,) if one else (gate, up):
-        if not t.is_cuda or t.dtype not in _HALVES or t.dim() != 2 or t.stride(1) != 1:
-            raise DQError(1, "dq_glu_quant: gate and up must be 2-D bf16/f16 CUDA tensors with adjacent columns")
-    if one and X.shape[1] % 2 != 0:
-        raise DQError(1, "dq_glu_quant: X must have an even number of columns")
-    if not one and (gate.shape != up.shape or gate.dtype != up.dtype or gate.device != up.device
-                    or (gate.shape[0] > 1 and gate.stride(0) != up.stride(0))):
-        raise DQError(1, "dq_glu_quant: gate and up must agree in shape, dtype, device and row stride")
-    return _call(gate.device, stream, _glu_quant, gate, up, one, col_scales, f, out, workspace, check)
-
-
-def _glu_quant(sp, gate, up, one, col_scales, f, out, workspace, check):
-    rows, cols = gate.shape
-    gp, upp = gate.data_ptr(), up.data_ptr()
-    if one:
-        cols //= 2
-        upp += 2 * cols
-    ld = gate.stride(0) if rows > 1 else cols + (-cols % 8)
-    bp = None if col_scales is None else _channel_vector(col_scales, cols, _HALVES, gate.device,
-                                                         "dq_glu_quant: col_scales")
-    out, struct = _row_outputs(out, gate, rows, cols, f, "dq_glu_quant: out")
-    workspace, wn = _workspace(workspace, out["codes"], ACT_WORKSPACE_BYTES if check or f.tensor_scale else 0,
-                               "dq_glu_quant")
-    st = _lib.dq_glu_quant(gp, upp, _DTYPES[gate.dtype], rows, cols, ld, bp,
-                           1 if col_scales is None else _DTYPES[col_scales.dtype], f.id, f.group, struct,
-                           None if workspace is None else workspace.data_ptr(), wn, sp)
-    if st != 0:
-        raise DQError(st, "dq_glu_quant")
-    if check:
-        _raise_device_status(workspace, sp, "dq_glu_quant")
-    if workspace is not None:
-        out["workspace"] = workspace
-    return out
+    gate, up = (X, None) if isinstance(X, torch.Tensor) else X
+    if not gate.is_cuda:
+        raise DQError(1, "dq_glu_quant: gate and up must be on a CUDA device")
+    return _call(gate.device, stream, m.glu_quant, gate, up, col_scales, f, out, workspace, bool(check))
 
 
 def dq_rtn(W: torch.Tensor, fmt, group: Optional[int] = None, col_dtype: Optional[str] = None, **kw) -> dict:

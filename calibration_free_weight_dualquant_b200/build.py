@@ -1,4 +1,4 @@
-"""Build libdq.so in-tree with nvcc for sm_100a.
+"""Build libdq.so in-tree with nvcc for sm_100a, and _dq_torch.so (argument marshalling) with the host compiler.
 
     python -m calibration_free_weight_dualquant_b200.build
 """
@@ -8,6 +8,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -15,6 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(OUT_DIR, "libdq.so")
+MARSHAL = os.path.join(OUT_DIR, "_dq_torch.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "dq_torch.cpp")
 SOURCES = ["dq_capi.cu", "dq_solver.cu", "dq_static.cu", "dq_act.cu", "dq_norm.cu", "dq_matmul.cu"]
 HEADERS = ["dq_device.cuh", "dq_fast.cuh", "dq_init.cuh", "dq_internal.h", "dq_iter.cuh", "dq_launch.h",
            "dq_tc.cuh"]
@@ -39,33 +43,55 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
-    objs = []
-    log = []
-    for src in SOURCES:
-        obj = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
-        cmd = [nvcc()] + ARCH_FLAGS + NVCC_FLAGS + ["-I", INCLUDE, "-I", CSRC, "-dc", "-o", obj,
-                                                     os.path.join(CSRC, src)]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        log.append(r.stdout + r.stderr)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError("nvcc failed on %s" % src)
-        objs.append(obj)
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc()] + ARCH_FLAGS + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs
+def _run(cmd, what: str) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("nvcc link failed")
-    os.replace(tmp, LIB)
-    with open(os.path.join(OUT_DIR, "ptxas.log"), "w") as f:
-        f.write("\n".join(log))
-    if verbose:
-        print("\n".join(log))
+        raise RuntimeError("%s failed" % what)
+    return r.stdout + r.stderr
+
+
+def build_marshal(force: bool = False) -> str:
+    """The CPython module of csrc/dq_torch.cpp, against torch's headers and libdq.so."""
+    deps = [MARSHAL_SOURCE, os.path.join(INCLUDE, "dq.h")]
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
+        return MARSHAL
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    includes = [sysconfig.get_paths()["include"], os.path.join(t, "include"),
+                os.path.join(t, "include", "torch", "csrc", "api", "include"), cuda, INCLUDE]
+    tmp = MARSHAL + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC"]
+    cmd += [a for d in includes for a in ("-I", d)]
+    cmd += ["-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, MARSHAL_SOURCE, "-o", tmp, "-L", OUT_DIR,
+            "-l:libdq.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch_python"]
+    _run(cmd, "g++ on dq_torch.cpp")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if force or _stale():
+        os.makedirs(OUT_DIR, exist_ok=True)
+
+        def compile_one(src):
+            obj = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
+            return obj, _run([nvcc()] + ARCH_FLAGS + NVCC_FLAGS + ["-I", INCLUDE, "-I", CSRC, "-dc", "-o", obj,
+                                                                  os.path.join(CSRC, src)], "nvcc on %s" % src)
+
+        with ThreadPoolExecutor(max(1, min(len(SOURCES), os.cpu_count() or 1))) as pool:
+            done = list(pool.map(compile_one, SOURCES))
+        tmp = LIB + ".tmp%d" % os.getpid()
+        _run([nvcc()] + ARCH_FLAGS + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + [obj for obj, _ in done], "nvcc link")
+        os.replace(tmp, LIB)
+        log = "\n".join(text for _, text in done)
+        with open(os.path.join(OUT_DIR, "ptxas.log"), "w") as f:
+            f.write(log)
+        if verbose:
+            print(log)
+    build_marshal(force)
     return LIB
 
 
