@@ -33,7 +33,7 @@
 namespace dq {
 
 constexpr int kGluThreads = 256;   // dq_glu_quant's block; two an SM
-constexpr int kGluMax = 512;       // ... and of a call that one CTA takes
+constexpr int kGluMax = 512;       // ... its largest, in a call that one cluster takes
 constexpr float kFltMax = 3.402823466e38f;
 
 struct RowProblem {
@@ -53,6 +53,7 @@ struct RowProblem {
   float* sT_out;
   double* rstd;           // NVFP4 norm: 1/rms of every row between the passes
   WsHeader* hdr;
+  int cluster;            // the grid is one cluster
 };
 
 __device__ __forceinline__ float2 h2_values(uint32_t u, int xdt) {
@@ -342,16 +343,21 @@ __device__ __forceinline__ void row_grid_barrier(WsHeader* hdr) {
   __syncthreads();
 }
 
+__device__ __forceinline__ void row_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Start of a kernel: everything before it in the stream is done.  A grid of one
-// CTA clears its own header.
-__device__ __forceinline__ void row_begin(WsHeader* hdr) {
+// CTA, or of one cluster, clears its own header (a cluster meets once more
+// before anything is written there).
+__device__ __forceinline__ void row_begin(const RowProblem& p) {
   griddep_launch_dependents();
   griddep_wait();
-  if (gridDim.x == 1 && hdr) {
-    if (threadIdx.x == 0) {
-      hdr->flags = 0;
-      hdr->gbar = 0;
-      hdr->amax_scaled = 0;
+  if ((gridDim.x == 1 || p.cluster) && p.hdr) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      p.hdr->flags = 0;
+      p.hdr->gbar = 0;
+      p.hdr->amax_scaled = 0;
     }
     __syncthreads();
   }
@@ -470,6 +476,20 @@ __device__ __forceinline__ unsigned long long amax_finish(const RowProblem& p, A
   if ((threadIdx.x & 31) == 0 && a.exact > 0.0) atomicMax(&all, (unsigned long long)__double_as_longlong(a.exact));
   __syncthreads();
   if (gridDim.x == 1) return all;
+  if (p.cluster) {
+    row_cluster_sync();
+    unsigned long long most = 0;
+    for (unsigned r = 0; r < gridDim.x; ++r) {
+      unsigned long long v;
+      asm volatile("{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %1, %2;\nld.shared::cluster.u64 %0, [a];\n}"
+                   : "=l"(v)
+                   : "r"(smem_u32(&all)), "r"(r)
+                   : "memory");
+      most = max(most, v);
+    }
+    row_cluster_sync();  // no CTA leaves while another reads its shared memory
+    return most;
+  }
   if (threadIdx.x == 0) atomicMax(&p.hdr->amax_scaled, all);
   row_grid_barrier(p.hdr);
   return *reinterpret_cast<volatile unsigned long long*>(&p.hdr->amax_scaled);
@@ -487,10 +507,13 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
   const int chunks = (int)(p.K / 16);
   const int trips = NC > 0 ? 1 : (chunks + nt - 1) / nt;
   const void* hsrc = p.y ? p.h : p.x;
-  row_begin(p.hdr);
+  row_begin(p);
   Amax amax;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
+  // NVFP4: a CTA with one row has it in registers in the second pass too
+  const bool kept = FMT == FMT_NVFP4 && NC > 0 && p.M <= gridDim.x;
+  double rstd = 0.0;
   V16 hv[N], rv[N];  // zeros for good where the thread has no chunk
 #pragma unroll
   for (int c = 0; c < N; ++c) hv[c] = rv[c] = zero16();
@@ -519,14 +542,13 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
     if (FMT == FMT_NVFP4 && pass == 1) {
       sT = tensor_scale(amax_finish<XDT, false>(p, amax));
-      if (ld_volatile(&p.hdr->flags) & kFlagTimeout) return;
+      if (gridDim.x > 1 && !p.cluster && (ld_volatile(&p.hdr->flags) & kFlagTimeout)) return;
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
     int64_t row0 = blockIdx.x * p.K + tid * 16;  // element of the thread's first chunk
 #pragma unroll 1
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, row0 += gridDim.x * p.K) {
-      double rstd;
       if (FMT != FMT_NVFP4 || pass == 0) {
         double s = 0.0;
 #pragma unroll 1
@@ -561,7 +583,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
         }
         rstd = row_rstd(s, red, p);
         if (FMT == FMT_NVFP4 && tid == 0) p.rstd[row] = rstd;
-      } else {
+      } else if (!kept) {
         rstd = p.rstd[row];
       }
       const float rs = (float)rstd;
@@ -573,7 +595,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
           const int i0 = (NC > 0 ? c : t) * nt;
           const bool on = tid + i0 < chunks;
           if (NC > 1 && (tid & ~31) + i0 >= chunks) break;  // the whole warp is past the row
-          if (NC == 0 || (FMT == FMT_NVFP4 && pass == 1)) hv[c] = on ? load16_again(hsrc, row0 + i0 * 16) : zero16();
+          if (NC == 0 || (FMT == FMT_NVFP4 && pass == 1 && !kept)) hv[c] = on ? load16_again(hsrc, row0 + i0 * 16) : zero16();
           if (NC == 0) get_gb(tid + i0);
           if (NC > 1) {
 #pragma unroll
@@ -675,36 +697,39 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
   // ... and as elements of the inputs and outputs, without and with a carry into the next row
   const int64_t din = drow * p.ld + dspan * 512, dout = drow * p.K + dspan * 512;
   const int64_t cin = p.ld - spans * 512, cout = p.K - spans * 512;
-  row_begin(p.hdr);
+  row_begin(p);
   Amax amax;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
   f2 b[8];
   int have = -1;
+  // NVFP4: a warp with one item has it in registers in the second pass too
+  const bool kept = FMT == FMT_NVFP4 && p.M * spans <= nw;
+  V16 gn = zero16(), un = zero16(), g1, u1;
 #pragma unroll 1
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
     if (FMT == FMT_NVFP4 && pass == 1) {
       sT = tensor_scale(amax_finish<XDT, true>(p, amax));
-      if (ld_volatile(&p.hdr->flags) & kFlagTimeout) return;
+      if (gridDim.x > 1 && !p.cluster && (ld_volatile(&p.hdr->flags) & kFlagTimeout)) return;
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
     int64_t row = w0 < nw ? w0 / spans : p.M;
     int span = (int)(w0 - row * spans);
     int64_t in = row * p.ld + (int64_t)span * 512 + lane * 16, at = row * p.K + (int64_t)span * 512 + lane * 16;
-    V16 gn = zero16(), un = zero16();
     auto read = [&]() {
       if (row < p.M && (int64_t)span * 512 + lane * 16 < p.K) {
         gn = load16(p.x, in, p.wide);
         un = load16(p.y, in, p.wide);
       }
     };
-    read();
+    if (!(kept && pass == 1)) read();
 #pragma unroll 1
     while (row < p.M) {
       const int64_t col = (int64_t)span * 512 + lane * 16, here = at;
       const bool on = col < p.K;
-      const V16 gv = gn, uv = un;
+      if (!(kept && pass == 1)) g1 = gn, u1 = un;
+      const V16 gv = g1, uv = u1;
       if (span != have) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) b[i] = 0ull;
@@ -721,7 +746,7 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
         in += cin;
         at += cout;
       }
-      read();
+      if (!kept) read();
       f2 v[8];
       bool far;
       glu_fast16<XDT>(gv, uv, b, v, far);
@@ -753,6 +778,11 @@ static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, boo
       (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
     return e;
   int grid = (int)(want < sms ? want : sms);
+  if (coop && grid > 1 && grid <= 8) {  // the CTAs of a cluster need no cooperative launch and no clearing
+    RowProblem one = p;
+    one.cluster = 1;
+    return launch_early(kern, (unsigned)grid, (unsigned)threads, smem, grid, st, one);
+  }
   if (want > sms) {
     int per_sm = 0;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return e;
@@ -792,8 +822,11 @@ static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
 template <int FMT, int XDT>
 static cudaError_t glu_launch(const RowProblem& p, int sms, cudaStream_t st) {
   const int64_t items = p.M * ((p.K + 511) / 512);
-  // NVFP4, few items: one CTA, whose two passes need no grid barrier and whose header no clearing
-  if (FMT == FMT_NVFP4 && items <= 2 * (kGluMax / 32)) return row_launch(k_glu<FMT, XDT>, p, true, 1, kGluMax, 0, sms, st);
+  // NVFP4, few items: one cluster with an item a warp, whose two passes need no grid barrier and whose header no clearing
+  if (FMT == FMT_NVFP4 && items <= 8 * (kGluMax / 32)) {
+    const int threads = items <= 32 ? 128 : (items <= 64 ? 256 : kGluMax);
+    return row_launch(k_glu<FMT, XDT>, p, true, (items + threads / 32 - 1) / (threads / 32), threads, 0, sms, st);
+  }
   return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, 0, sms, st);
 }
 
