@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   using G = MmGeo<FMT, BN>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kMmMaxStages], empty[kMmMaxStages], full_s[2], empty_s[2], acc_full;
+  __shared__ uint64_t full_t[kMmMaxStages], empty[kMmMaxStages], full_s[2], empty_s[2], acc_full, given_up;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
   unsigned char* scales = ring + l.stages * G::kStage;
@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
       mbar_init(&empty_s[i], 1);
     }
     mbar_init(&acc_full, 1);
+    mbar_init(&given_up, 1);
     mbar_fence_init();
   }
   if (warp == 1) tc_alloc<1, G::kAlloc>(smem_u32(&tmem_base));
@@ -416,7 +417,8 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     if (elect_one()) {
       MmSlot at;
       unsigned piece = 0;
-      for (int it = 0; it < n; ++it) {
+      int it = 0;
+      for (; it < n; ++it) {
         const int kt = (int)k0 + it, u = kt % F::kPiece;
         if ((it == 0 || u == 0) && !mm_wait(&full_s[piece & 1], (piece >> 1) & 1, flags)) break;
         if (!mm_wait(&full_t[at.slot], at.phase, flags)) break;
@@ -437,7 +439,12 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         if (u == F::kPiece - 1) tc_commit<1>(&empty_s[piece++ & 1]);
         at.next(l.stages);
       }
-      tc_commit<1>(&acc_full);
+      if (it == n) {
+        tc_commit<1>(&acc_full);
+      } else {  // the tile is not finished, so its readers' wait runs out too; what was issued ends before the CTA does
+        tc_commit<1>(&given_up);
+        mbar_drain(&given_up, 0);
+      }
     }
   } else {
     const bool of_w = (warp & 1) == 0;
@@ -627,7 +634,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using G = PairGeo<FMT>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kPairStages], empty[kPairStages], full_s[2], empty_s[2], acc_full, acc_empty;
+  __shared__ uint64_t full_t[kPairStages], empty[kPairStages], full_s[2], empty_s[2], acc_full, acc_empty,
+      given_up;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
   unsigned char* scales = ring + kPairStages * G::kStage;
@@ -649,6 +657,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&empty_s[i], 1);
     }
     mbar_init(&acc_full, 1);
+    mbar_init(&given_up, 1);
     mbar_init(&acc_empty, 2 * kPairEpilogue);
     mbar_fence_init();
   }
@@ -723,7 +732,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (u == F::kPiece - 1 || kt == k1 - 1) tc_commit<2>(&empty_s[piece++ & 1], leader);
           at.next(kPairStages);
         }
-        tc_commit<2>(&acc_full, leader);
+        if (ok) tc_commit<2>(&acc_full, leader);
+      }
+      if (!ok) {  // as above
+        tc_commit<2>(&given_up, leader);
+        mbar_drain(&given_up, 0);
       }
     }
   } else if (warp >= 10) {
@@ -998,7 +1011,8 @@ extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* 
   if (format != DQ_NVFP4 && format != DQ_MXFP4 && format != DQ_MXFP8) return DQ_EUNSUPPORTED;
   if (group != (format == DQ_NVFP4 ? 16 : 32)) return DQ_EUNSUPPORTED;
   if (y_dtype < DQ_F32 || y_dtype > DQ_F16) return DQ_EINVAL;
-  if (tokens > INT_MAX - 256 || rows > INT_MAX - 256 || cols > INT_MAX - 256) return DQ_EUNSUPPORTED;
+  // a tile's sum must end well within the waits' limit of 1 s: 2^27 columns take 0.4 s
+  if (tokens > INT_MAX - 256 || rows > INT_MAX - 256 || cols > ((int64_t)1 << 27)) return DQ_EUNSUPPORTED;
   if ((tokens + 63) / 64 * ((rows + 63) / 64) > INT_MAX) return DQ_EUNSUPPORTED;
   if (!X || !W || !X->codes || !X->block_scales || !W->codes || !W->block_scales || !Y) return DQ_EINVAL;
   if (format == DQ_NVFP4 && (!X->tensor_scale || !W->tensor_scale || (uintptr_t)X->tensor_scale % 4 != 0 ||

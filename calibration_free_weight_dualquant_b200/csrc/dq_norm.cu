@@ -839,7 +839,7 @@ static int row_check(int64_t rows, int64_t cols, int x_dtype, const void* col_sc
   if (group != (format == DQ_NVFP4 ? 16 : 32)) return DQ_EUNSUPPORTED;
   if (x_dtype != DQ_BF16 && x_dtype != DQ_F16) return DQ_EUNSUPPORTED;
   if (col_scales && col_dtype != DQ_BF16 && col_dtype != DQ_F16) return DQ_EUNSUPPORTED;
-  if (rows > ((int64_t)1 << 40) / cols) return DQ_EUNSUPPORTED;
+  if (rows > ((int64_t)1 << 40) / cols || cols > INT_MAX) return DQ_EUNSUPPORTED;
   if ((uintptr_t)col_scales % 2 != 0) return DQ_EINVAL;
   if (!out || !out->codes || !out->block_scales || (uintptr_t)out->codes % 8 != 0 ||
       (format == DQ_NVFP4 && !out->tensor_scale) || (uintptr_t)out->tensor_scale % 4 != 0)
@@ -871,7 +871,7 @@ static void row_fill(RowProblem* p, int64_t rows, int64_t cols, const void* col_
 }  // namespace dq
 
 extern "C" size_t dq_norm_workspace_bytes(int64_t rows, int64_t cols, int format, int group) {
-  if (rows <= 0 || cols <= 0 || group <= 0 || cols % group != 0 || rows > ((int64_t)1 << 40) / cols) return 0;
+  if (rows <= 0 || cols <= 0 || group <= 0 || cols % group != 0 || rows > ((int64_t)1 << 40) / cols || cols > INT_MAX) return 0;
   if (format != DQ_NVFP4 && format != DQ_MXFP4 && format != DQ_MXFP8) return 0;
   if (group != (format == DQ_NVFP4 ? 16 : 32)) return 0;
   return DQ_ACT_WORKSPACE_BYTES + (format == DQ_NVFP4 ? (size_t)rows * sizeof(double) : 0);

@@ -312,8 +312,8 @@ int dq_act_quant(const void* X, int x_dtype, int64_t rows, int64_t cols, const v
  * Y  [tokens][rows], densely packed, y_dtype DQ_F32, DQ_BF16 or DQ_F16; it must
  *    not overlap the operands.
  * Formats DQ_NVFP4, DQ_MXFP4 and DQ_MXFP8; the integer grids return
- * DQ_EUNSUPPORTED.  cols is a multiple of the group, the other sizes are any
- * from 1.  Products of codes and scales are exact, sums are fp32 and rounded
+ * DQ_EUNSUPPORTED.  cols is a multiple of the group and at most
+ * 2^27, the other sizes are any from 1.  Products of codes and scales are exact, sums are fp32 and rounded
  * once to y_dtype; a value beyond its range becomes an infinity.  A NaN block
  * scale (E8M0 0xFF, E4M3 0x7F) makes its row's outputs NaN and no others.  The
  * order of a sum depends on the shape alone, so equal calls give equal bits.

@@ -196,6 +196,36 @@ def test_matmul_of_the_solvers_outputs():
     assert (y.double() - full).norm() / full.norm() < 0.25
 
 
+@pytest.mark.parametrize("fmt,wl", [("mxfp4", "mxfp4_g32_downproj_4096x14336"), ("mxfp8", "mxfp8_g32_downproj_4096x14336"),
+                                    ("nvfp4", "nvfp4_g16_gateup_14336x4096")])
+def test_mlp_block_of_solved_weights(fmt, wl):
+    """norm, gate/up product, glu, down product on dq_solve's weights and column scales: each step against the fp64
+    definition on what the one before stored."""
+    tokens, cols, inter = 40, 512, 768
+    wl = synth.WORKLOADS[wl]
+    w1, w2 = synth.make_weight(wl, 2 * inter, cols, seed=1).cuda(), synth.make_weight(wl, cols, inter, seed=2).cuda()
+    q1, q2 = (binding.dq_solve(w, fmt, wl.group, 4, wl.col_dtype) for w in (w1, w2))
+    x = synth.make_activations(tokens, cols, seed=3).cuda()
+    r = synth.make_activations(tokens, cols, seed=4).cuda()
+    g = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    n = binding.dq_norm_quant(x, g, q1["col_scales"], fmt, residual=r)
+    h, x64 = ref.norm(x, r, g, q1["col_scales"], 1e-5)
+    assert torch.equal(n["residual"].cpu(), h)
+    same_codes(n, ref.quantize(x64, fmt), fmt)
+    gu = binding.dq_matmul(n, q1, fmt)
+    check(gu, n, q1, fmt, "gate and up")
+    a = binding.dq_glu_quant(gu, q2["col_scales"], fmt)
+    same_codes(a, ref.quantize(ref.glu(gu[:, :inter], gu[:, inter:], q2["col_scales"]), fmt), fmt)
+    y = binding.dq_matmul(a, q2, fmt, out_dtype=torch.float32)
+    check(y, a, q2, fmt, "down")
+
+
+def same_codes(got: dict, want: dict, fmt: str):
+    for k in ("codes", "block_scales"):
+        assert np.array_equal(got[k].cpu().numpy(), want[k]), k
+    assert fmt != "nvfp4" or np.float32(got["tensor_scale"].cpu()[0]) == want["tensor_scale"]
+
+
 def test_matmul_captured_and_replayed():
     x, w = case(3, 300, 1024, "nvfp4", 81)
     xd, wd = ref.to(x, "cuda"), ref.to(w, "cuda")
@@ -212,6 +242,56 @@ def test_matmul_captured_and_replayed():
     g.replay()
     torch.cuda.synchronize()
     check(out, x2, w, "nvfp4")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("tokens,rows,cols", [(300, 1024, 4096), (2300, 2500, 4096), (40, 512, 2048)])
+def test_matmul_of_many_tokens_captured_and_replayed(fmt, tokens, rows, cols):
+    """Clusters, and whole waves followed by a launch over the rest, in a graph of two calls in a row."""
+    x, w = case(tokens, rows, cols, fmt, 83)
+    xd, wd = ref.to(x, "cuda"), ref.to(w, "cuda")
+    outs = [torch.empty(tokens, rows, dtype=torch.float32, device="cuda") for _ in range(2)]
+    binding.dq_matmul(xd, wd, fmt, out=outs[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for o in outs:
+            binding.dq_matmul(xd, wd, fmt, out=o, check=False)
+    x2 = ref.random_quantized(tokens, cols, fmt, 84)
+    for k in xd:
+        xd[k].copy_(x2[k])
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1])
+    check(outs[1], x2, w, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_matmul_without_workspace_and_with_one(fmt):
+    x, w = case(9, 300, 512, fmt, 85)
+    xd, wd = ref.to(x, "cuda"), ref.to(w, "cuda")
+    ws = torch.randint(0, 256, (256,), dtype=torch.uint8, device="cuda")  # its contents on entry do not matter
+    a = binding.dq_matmul(xd, wd, fmt, out_dtype=torch.float32, workspace=ws)
+    b = binding.dq_matmul(xd, wd, fmt, out_dtype=torch.float32, check=False)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp8"])
+def test_matmul_offsets_beyond_32_bits(fmt):
+    """Weights of more than 2^32 bytes (MXFP8) or elements (NVFP4), outputs of more than 2^31 bytes: the last rows."""
+    cols, rows = 4096, 2 ** 20 + 300
+    codes = torch.zeros(rows, cols if fmt == "mxfp8" else cols // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(rows, cols // ref.GROUP[fmt], dtype=torch.uint8, device="cuda")
+    x, tail = case(600, 300, cols, fmt, 87)
+    codes[-300:] = tail["codes"].cuda()
+    scales[-300:] = tail["block_scales"].cuda()
+    big = {"codes": codes, "block_scales": scales, "tensor_scale": tail["tensor_scale"].cuda()}
+    for tokens in (3, 600):
+        part = {"codes": x["codes"][:tokens], "block_scales": x["block_scales"][:tokens], "tensor_scale": x["tensor_scale"]}
+        y = binding.dq_matmul(ref.to(part, "cuda"), big, fmt, out_dtype=torch.float32)
+        assert not y[:, :-300].any()
+        check(y[:, -300:].contiguous(), part, tail, fmt)
+        del y
 
 
 def test_matmul_on_two_streams_at_once():

@@ -148,6 +148,37 @@ def test_norm_in_place_residual(fmt, where):
     same(got, x64, fmt)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_rows_offsets_beyond_32_bits(fmt):
+    """More than 2^31 elements: the last rows are what they are alone."""
+    cols, rows = 4096, 2 ** 19 + 40
+    x, r, w, b = norm_case(40, cols, torch.bfloat16, torch.bfloat16, 43)
+    big = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    big[-40:] = x.cuda()
+    got = binding.dq_norm_quant(big, w.cuda(), b.cuda(), fmt)
+    alone = binding.dq_norm_quant(x.cuda(), w.cuda(), b.cuda(), fmt)
+    for k in ("codes", "block_scales"):
+        assert torch.equal(got[k][-40:], alone[k]), k
+    assert not got["codes"][:-40].any() and (got["block_scales"][:-40] == 127).all()
+    got = binding.dq_glu_quant((big, big), b.cuda(), fmt)
+    alone = binding.dq_glu_quant((x.cuda(), x.cuda()), b.cuda(), fmt)
+    for k in ("codes", "block_scales"):
+        assert torch.equal(got[k][-40:], alone[k]), k
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("tokens", [1, 2, 5, 8, 9, 40])
+def test_rows_workspace_contents_do_not_matter(fmt, tokens):
+    """One CTA, one cluster and a whole grid, each on a workspace full of anything, twice."""
+    x, r, w, b = norm_case(tokens, 512, torch.bfloat16, torch.bfloat16, 47)
+    gx, gb = glu_case(tokens, 1024, torch.bfloat16, 48)
+    ws = torch.randint(0, 256, (256 + 8 * tokens,), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        run_norm(x, r, w, b, fmt, workspace=ws)
+        ws.random_(0, 256)
+        same(binding.dq_glu_quant(gx.cuda(), gb.cuda(), fmt, workspace=ws), ref.glu(gx[:, :1024], gx[:, 1024:], gb), fmt)
+
+
 def glu_case(tokens, cols, dtype, seed):
     rng = torch.Generator().manual_seed(seed)
     x = (3 * torch.randn(tokens, 2 * cols, generator=rng)).to(dtype)

@@ -36,6 +36,7 @@ def matmul(lib, tokens=4, rows=8, cols=64, fmt=3, group=32, y=FAKE, dt=1, ws=FAK
     (dict(dt=0, y=FAKE + 2), 1), (dict(ws=FAKE + 16), 1), (dict(nbytes=255), 3),
     (dict(X=outs(codes=None)), 1), (dict(W=outs(scales=None)), 1), (dict(fmt=2, group=16, X=outs(sT=None)), 1),
     (dict(fmt=2, group=16, W=outs(sT=FAKE + 2)), 1), (dict(tokens=2 ** 31), 2), (dict(tokens=2 ** 30, rows=2 ** 30), 2),
+    (dict(cols=2 ** 27 + 32), 2),
 ])
 def test_matmul_refusals(lib, kw, status):
     assert matmul(lib, **kw) == status
@@ -54,7 +55,7 @@ def norm(lib, X=FAKE, r=None, xdt=1, rows=2, cols=64, g=FAKE, eps=1e-5, b=FAKE, 
     (dict(r=FAKE, ro=FAKE + 4), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
     (dict(out=outs(codes=FAKE + 4)), 1), (dict(out=outs(scales=None)), 1),
     (dict(fmt=2, group=16, out=outs(sT=None)), 1), (dict(fmt=2, group=16, ws=None), 1), (dict(ws=FAKE + 128), 1), (dict(nbytes=255), 3),
-    (dict(fmt=2, group=16, nbytes=256), 3), (dict(rows=2 ** 40), 2),
+    (dict(fmt=2, group=16, nbytes=256), 3), (dict(rows=2 ** 40), 2), (dict(rows=1, cols=2 ** 31), 2),
 ])
 def test_norm_refusals(lib, kw, status):
     assert norm(lib, **kw) == status
@@ -77,7 +78,7 @@ def glu(lib, gate=FAKE, up=FAKE, xdt=1, rows=2, cols=64, ld=128, b=FAKE, bdt=1, 
     (dict(rows=0), 1), (dict(cols=72), 1), (dict(ld=56), 1), (dict(ld=132), 1), (dict(gate=None), 1), (dict(up=None), 1),
     (dict(gate=FAKE + 2), 1), (dict(up=FAKE + 8), 1), (dict(xdt=0), 2), (dict(fmt=1), 2), (dict(fmt=2), 2),
     (dict(b=FAKE + 1), 1), (dict(bdt=0), 2), (dict(out=outs(codes=None)), 1), (dict(ws=FAKE + 8), 1), (dict(nbytes=0), 3),
-    (dict(fmt=2, group=16, out=outs(sT=None)), 1), (dict(rows=2 ** 32, ld=2 ** 20), 1),
+    (dict(fmt=2, group=16, out=outs(sT=None)), 1), (dict(rows=2 ** 32, ld=2 ** 20), 1), (dict(rows=1, cols=2 ** 31, ld=2 ** 31), 2),
 ])
 def test_glu_refusals(lib, kw, status):
     assert glu(lib, **kw) == status
