@@ -632,6 +632,47 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
 // of a row's items where there are enough, so a warp keeps its columns and
 // their scales.
 
+// A lane's 16 column scales and their products with 16-bit values, exact in fp32:
+// as stored, multiplied by mixed-precision fma, where the types agree.
+template <bool BSAME>
+struct GluCols {
+  uint32_t w[BSAME ? 8 : 1];
+  f2 f[BSAME ? 1 : 8];
+  __device__ __forceinline__ void load(const RowProblem& p, int64_t col, bool on) {
+    if (BSAME) {
+      const uint16_t* b = reinterpret_cast<const uint16_t*>(p.b_store) + col;
+#pragma unroll
+      for (int i = 0; i < (BSAME ? 8 : 1); ++i) w[i] = on ? (uint32_t)b[2 * i] | (uint32_t)b[2 * i + 1] << 16 : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < (BSAME ? 1 : 8); ++i) f[i] = 0ull;
+      if (on) b16_values(p, col, f);
+    }
+  }
+  __device__ __forceinline__ void times(const V16& v, int xdt, f2* x) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (BSAME) {
+        float lo, hi;
+        if (xdt == DT_BF16)
+          asm("{\n.reg .b16 x0, x1, b0, b1;\nmov.b32 {x0, x1}, %2;\nmov.b32 {b0, b1}, %3;\n"
+              "fma.rn.f32.bf16 %0, x0, b0, 0f80000000;\nfma.rn.f32.bf16 %1, x1, b1, 0f80000000;\n}"
+              : "=f"(lo), "=f"(hi)
+              : "r"(v.u[i]), "r"(w[BSAME ? i : 0]));
+        else
+          asm("{\n.reg .b16 x0, x1, b0, b1;\nmov.b32 {x0, x1}, %2;\nmov.b32 {b0, b1}, %3;\n"
+              "fma.rn.f32.f16 %0, x0, b0, 0f80000000;\nfma.rn.f32.f16 %1, x1, b1, 0f80000000;\n}"
+              : "=f"(lo), "=f"(hi)
+              : "r"(v.u[i]), "r"(w[BSAME ? i : 0]));
+        x[i] = pk(lo, hi);
+      } else {
+        const float2 a = h2_values(v.u[i], xdt);
+        x[i] = mul2(pk(a.x, a.y), f[BSAME ? 0 : i]);
+      }
+    }
+  }
+};
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -664,14 +705,14 @@ __device__ __forceinline__ void range16(const V16& v, float& lo, float& hi) {
 // leaves that bound; an up * b that overflows shows as an infinity or a NaN.
 // (Otherwise an up * b below the normal range gives |x'| < 2^-86: a zero code in
 // every group whose scale the fast path settles.)
-template <int XDT>
-__device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const f2* b, f2* v, bool& far) {
+template <int XDT, bool BSAME>
+__device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const GluCols<BSAME>& b, f2* v, bool& far) {
   float lo, hi;
   range16<XDT>(gv, lo, hi);
   far = !(lo >= -80.f && hi <= 0x1p40f);
   f2 g[8], u[8];
   pairs16<XDT>(gv, g);
-  pairs16<XDT>(uv, u);
+  b.times(uv, XDT, u);
   // log2(e) as the sum of two fp32 numbers
   const f2 l1 = splat(1.44269502f), m1 = splat(-1.44269502f), l2 = splat((float)(1.4426950408889634 - (double)1.44269502f));
 #pragma unroll
@@ -682,11 +723,11 @@ __device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const f
     e = fma2(e, mul2(r, splat(-0.693147181f)), e);
     const f2 d = add2(e, splat(1.f));
     const f2 s = pk(rcp_approx(lo_of(d)), rcp_approx(hi_of(d)));
-    v[i] = mul2(mul2(g[i], s), mul2(u[i], b[i]));
+    v[i] = mul2(mul2(g[i], s), u[i]);
   }
 }
 
-template <int FMT, int XDT>
+template <int FMT, int XDT, bool BSAME>
 __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowProblem p) {
   const int lane = threadIdx.x & 31;
   const int64_t spans = (p.K + 511) / 512;  // 512-column pieces of a row
@@ -701,11 +742,11 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
   Amax amax;
   float sT = 1.f, isT = 1.f;
   bool sT_ok = true, bad = false;
-  f2 b[8];
+  GluCols<BSAME> b;
   int have = -1;
   // NVFP4: a warp with one item has it in registers in the second pass too
   const bool kept = FMT == FMT_NVFP4 && p.M * spans <= nw;
-  V16 gn = zero16(), un = zero16(), g1, u1;
+  V16 g0 = zero16(), u0 = zero16(), g1 = zero16(), u1 = zero16();  // two items in turn: no copies of registers
 #pragma unroll 1
   for (int pass = FMT == FMT_NVFP4 ? 0 : 1; pass < 2; ++pass) {
     if (FMT == FMT_NVFP4 && pass == 1) {
@@ -717,23 +758,18 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
     int64_t row = w0 < nw ? w0 / spans : p.M;
     int span = (int)(w0 - row * spans);
     int64_t in = row * p.ld + (int64_t)span * 512 + lane * 16, at = row * p.K + (int64_t)span * 512 + lane * 16;
-    auto read = [&]() {
+    auto read = [&](V16& g, V16& u) {
       if (row < p.M && (int64_t)span * 512 + lane * 16 < p.K) {
-        gn = load16(p.x, in, p.wide);
-        un = load16(p.y, in, p.wide);
+        g = load16(p.x, in, p.wide);
+        u = load16(p.y, in, p.wide);
       }
     };
-    if (!(kept && pass == 1)) read();
-#pragma unroll 1
-    while (row < p.M) {
+    // works on (gv, uv), the item at row and span, and reads the next one
+    auto step = [&](const V16& gv, const V16& uv, V16& g, V16& u) {
       const int64_t col = (int64_t)span * 512 + lane * 16, here = at;
       const bool on = col < p.K;
-      if (!(kept && pass == 1)) g1 = gn, u1 = un;
-      const V16 gv = g1, uv = u1;
       if (span != have) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = 0ull;
-        if (on) b16_values(p, col, b);
+        b.load(p, col, on);
         have = span;
       }
       row += drow;
@@ -746,10 +782,10 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
         in += cin;
         at += cout;
       }
-      if (!kept) read();
+      if (!kept) read(g, u);
       f2 v[8];
       bool far;
-      glu_fast16<XDT>(gv, uv, b, v, far);
+      glu_fast16<XDT, BSAME>(gv, uv, b, v, far);
       if (FMT == FMT_NVFP4 && pass == 0) {
         // values that are not finite have no share in the tensor scale
         amax_add<XDT, true>(p, amax, absmax16(v), here, on && !zero_bits16(gv) && !zero_bits16(uv), far, 0.0);
@@ -758,6 +794,13 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
         bad |= quant_store16<FMT, XDT, true>(p, here, on, v, 1.25f * 0x1p-20f, sT, isT,
                                              [&] { return zero_bits16(gv) || zero_bits16(uv); }, !sT_ok || far, 0.0);
       }
+    };
+    if (!(kept && pass == 1)) read(g0, u0);
+#pragma unroll 1
+    while (row < p.M) {
+      step(g0, u0, g1, u1);
+      if (row >= p.M) break;
+      step(g1, u1, g0, u0);
     }
   }
   if (blockIdx.x == 0 && threadIdx.x == 0 && p.sT_out) *p.sT_out = sT;
@@ -821,13 +864,14 @@ static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
 
 template <int FMT, int XDT>
 static cudaError_t glu_launch(const RowProblem& p, int sms, cudaStream_t st) {
+  void (*kern)(RowProblem) = p.b_store && p.col_dt == XDT ? k_glu<FMT, XDT, true> : k_glu<FMT, XDT, false>;
   const int64_t items = p.M * ((p.K + 511) / 512);
   // NVFP4, few items: one cluster with an item a warp, whose two passes need no grid barrier and whose header no clearing
   if (FMT == FMT_NVFP4 && items <= 8 * (kGluMax / 32)) {
     const int threads = items <= 32 ? 128 : (items <= 64 ? 256 : kGluMax);
-    return row_launch(k_glu<FMT, XDT>, p, true, (items + threads / 32 - 1) / (threads / 32), threads, 0, sms, st);
+    return row_launch(kern, p, true, (items + threads / 32 - 1) / (threads / 32), threads, 0, sms, st);
   }
-  return row_launch(k_glu<FMT, XDT>, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, 0, sms, st);
+  return row_launch(kern, p, FMT == FMT_NVFP4, (items + 7) / 8, kGluThreads, 0, sms, st);
 }
 
 // Checks shared by the two entry points.
