@@ -374,7 +374,7 @@ __device__ __forceinline__ float tensor_scale(unsigned long long bits) {
 // ---------------------------------------------------------------------------
 // dq_norm_quant: a CTA takes rows grid-stride, thread t the 16-element chunks
 // t, t + blockDim, ...  With NC > 0 a thread has at most NC chunks and keeps its
-// part of the row in registers; with NC = 0 (rows longer than 8 x 256 chunks)
+// part of the row in registers; with NC = 0 (rows longer than 4 x 512 chunks)
 // the stored row is read again after the sum.  The sum of squares is held in
 // fp64.
 
@@ -495,10 +495,10 @@ __device__ __forceinline__ unsigned long long amax_finish(const RowProblem& p, A
   return *reinterpret_cast<volatile unsigned long long*>(&p.hdr->amax_scaled);
 }
 
-__host__ __device__ constexpr int norm_threads(int nc) { return nc == 1 ? 512 : 256; }
+__host__ __device__ constexpr int norm_threads(int nc) { return nc == 1 || nc == 4 ? 512 : 256; }
 
 template <int FMT, int XDT, int NC>
-__global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(const __grid_constant__ RowProblem p) {
+__global__ void __launch_bounds__(norm_threads(NC), NC == 2 ? 3 : 1) k_norm(const __grid_constant__ RowProblem p) {
   __shared__ double red[33];
   // g b of the thread's own chunks (NC > 1), 16-byte pieces [c][piece][thread]: written and read by one thread
   extern __shared__ uint4 gb_kept[];
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
 #pragma unroll 1
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, row0 += gridDim.x * p.K) {
       if (FMT != FMT_NVFP4 || pass == 0) {
-        double s = 0.0;
+        double s[4] = {0.0, 0.0, 0.0, 0.0};  // four chains of additions
 #pragma unroll 1
         for (int t = 0; t < trips; ++t) {
 #pragma unroll
@@ -576,12 +576,12 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 1 ? 1 : 2) k_norm(cons
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float2 h = h2_values(hv[c].u[i], XDT);
-              s = fma((double)h.x, (double)h.x, s);
-              s = fma((double)h.y, (double)h.y, s);
+              s[2 * (i & 1)] = fma((double)h.x, (double)h.x, s[2 * (i & 1)]);
+              s[2 * (i & 1) + 1] = fma((double)h.y, (double)h.y, s[2 * (i & 1) + 1]);
             }
           }
         }
-        rstd = row_rstd(s, red, p);
+        rstd = row_rstd((s[0] + s[1]) + (s[2] + s[3]), red, p);
         if (FMT == FMT_NVFP4 && tid == 0) p.rstd[row] = rstd;
       } else if (!kept) {
         rstd = p.rstd[row];
@@ -841,23 +841,23 @@ static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, boo
   return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(threads), args, smem, st);
 }
 
-// Few rows: a chunk a thread, for latency.  From 4 rows an SM on: CTAs of two
-// warps or little more with up to 4 chunks a thread, which leave each other less
-// idle at the row's two barriers (8192 x 4096 MXFP8: 74 us with 1 chunk a
-// thread, 62 with 2, 58 with 4, 77 with 8, whose registers halve the warps).
+// Few rows: a chunk a thread, for latency.  From 4 rows an SM on: 2 chunks a
+// thread at 80 registers, for 24 warps an SM (8192 x 4096 MXFP8: 53 us with 1
+// chunk a thread, 50 with 2, 51 with 4 at 126 registers).  What bounds it then is
+// latency, not the memory: bringing the next row into shared memory meanwhile
+// took longer (56 us).
 template <int FMT, int XDT>
 static cudaError_t norm_launch(const RowProblem& p, int sms, cudaStream_t st) {
   const int64_t chunks = p.K / 16;
   int nc, threads;
-  if (p.M >= 4 * (int64_t)sms)
-    nc = chunks <= 64 ? 1 : (chunks <= 128 ? 2 : (chunks <= 4 * 256 ? 4 : (chunks <= 8 * 256 ? 8 : 0)));
+  if (chunks > 512)
+    nc = chunks <= 4 * 512 ? 4 : 0;
   else
-    nc = chunks <= 512 ? 1 : (chunks <= 8 * 256 ? 8 : 0);
+    nc = p.M >= 4 * (int64_t)sms ? 2 : 1;
   threads = nc == 0 ? 256 : (int)(((chunks + nc - 1) / nc + 31) / 32 * 32);
   void (*kern)(RowProblem) = nc == 1   ? k_norm<FMT, XDT, 1>
                              : nc == 2 ? k_norm<FMT, XDT, 2>
                              : nc == 4 ? k_norm<FMT, XDT, 4>
-                             : nc == 8 ? k_norm<FMT, XDT, 8>
                                        : k_norm<FMT, XDT, 0>;
   return row_launch(kern, p, FMT == FMT_NVFP4, p.M, threads, nc > 1 ? (size_t)nc * threads * 64 : 0, sms, st);
 }
