@@ -288,20 +288,36 @@ struct MmSlot {
 
 // Scales travel in pieces of 32 bytes a row, one memory sector: the scales of
 // 2, 4 or 8 K tiles.  (Read a K tile at a time, the same sector would come from
-// L2 every time, and every K tile would cost its own barriers.)  The piece ring
-// has two slots and each 128-row block two warps that take turns, warp t filling
-// slot t, so that one reads while the other waits or writes: the proxy fence
-// that publishes a piece waits for the warp's own reads in flight.
+// L2 every time, and every K tile would cost its own barriers.)  Each 128-row
+// block has two warps that take turns, so that one reads while the other waits
+// or writes: the proxy fence that publishes a piece waits for the warp's own
+// reads in flight.  A slot is free when its piece's multiply-adds are done, and
+// filling it takes longer than those of one K tile, so two slots do while a
+// piece is 4 or 8 tiles, and the pairs' kernel has three for NVFP4's pieces of
+// two (8192 x 14336 x 4096: 215 us against 222).  The kernel of few tokens waits
+// for the weight's bytes and leaves the room to them.  (A warp may wait for a
+// slot's barrier by parity: when it filled piece p - 2 it waited for p - 2 - SLOTS,
+// so the phase two before the one that it waits for now is over.)
+constexpr int kScaleSlots = 2;
 struct ScaleTurn {
   int turn;            // 0 or 1
   unsigned piece = 0;  // pieces of the block so far, over all its tiles
 };
+// Slot and phase of a piece's use of the ring, for those who take every piece.
+template <int SLOTS>
+struct ScaleSlot {
+  int slot = 0;
+  unsigned phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == SLOTS) slot = 0, phase ^= 1;
+  }
+};
 
-// A warp's share of one block's scales of the K tiles k0 .. k0 + n - 1.  Slot t
-// of the ring starts at ring + t * slot_bytes; the words of K tile u of a piece
+// A warp's share of one block's scales of the K tiles k0 .. k0 + n - 1.  Slot i
+// of the ring starts at ring + i * slot_bytes; the words of K tile u of a piece
 // and scale word j are the 512-byte block u * kAtoms + j, block_bytes apart.
 // PAIR: the arrival goes to the cluster's CTA `leader`.
-template <bool PAIR, int U>
+template <bool PAIR, int SLOTS, int U>
 __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0, int64_t rows,
                                            int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes, int block_bytes,
                                            uint64_t* full, uint64_t* empty, unsigned* flags, uint32_t leader) {
@@ -312,8 +328,9 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
     if ((int)(t.piece & 1) != t.turn) continue;
     uint32_t w[4][8];
     load_scales<U>(s, row0, rows, nb, piece, w);
-    if (!__all_sync(0xffffffffu, mm_wait(&empty[t.turn], ((t.piece >> 1) & 1) ^ 1, flags))) return false;
-    unsigned char* dst = ring + t.turn * slot_bytes + lane * 16;
+    const unsigned use = t.piece / SLOTS, slot = t.piece - use * SLOTS;
+    if (!__all_sync(0xffffffffu, mm_wait(&empty[slot], (use & 1) ^ 1, flags))) return false;
+    unsigned char* dst = ring + slot * slot_bytes + lane * 16;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       *reinterpret_cast<uint4*>(dst + j * block_bytes) = make_uint4(w[0][j], w[1][j], w[2][j], w[3][j]);
@@ -321,21 +338,21 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
     __syncwarp();
     if (lane == 0) {
       if (PAIR)
-        mbar_arrive_cluster(&full[t.turn], leader);
+        mbar_arrive_cluster(&full[slot], leader);
       else
-        mbar_arrive(&full[t.turn]);
+        mbar_arrive(&full[slot]);
     }
   }
   return true;
 }
 // `unit`: the largest power of two (32 at most) that divides the scales' address
 // and the row's length.
-template <bool PAIR>
+template <bool PAIR, int SLOTS>
 __device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0,
                                            int64_t rows, int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes,
                                            int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags, uint32_t leader) {
 #define DQ_SCALE_LOOP(U) \
-  scale_loop<PAIR, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, flags, leader)
+  scale_loop<PAIR, SLOTS, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, flags, leader)
   if (unit == 32) return DQ_SCALE_LOOP(32);
   if (unit == 16) return DQ_SCALE_LOOP(16);
   return DQ_SCALE_LOOP(1);
@@ -356,7 +373,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   using G = MmGeo<FMT, BN>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kMmMaxStages], empty[kMmMaxStages], full_s[2], empty_s[2], acc_full, given_up;
+  __shared__ uint64_t full_t[kMmMaxStages], empty[kMmMaxStages], full_s[kScaleSlots], empty_s[kScaleSlots], acc_full, given_up;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
   unsigned char* scales = ring + l.stages * G::kStage;
@@ -374,7 +391,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
       mbar_init(&full_t[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kScaleSlots; ++i) {
       mbar_init(&full_s[i], 2);
       mbar_init(&empty_s[i], 1);
     }
@@ -416,15 +433,15 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   } else if (warp == 1) {
     if (elect_one()) {
       MmSlot at;
-      unsigned piece = 0;
+      ScaleSlot<kScaleSlots> piece;
       int it = 0;
       for (; it < n; ++it) {
         const int kt = (int)k0 + it, u = kt % F::kPiece;
-        if ((it == 0 || u == 0) && !mm_wait(&full_s[piece & 1], (piece >> 1) & 1, flags)) break;
+        if ((it == 0 || u == 0) && !mm_wait(&full_s[piece.slot], piece.phase, flags)) break;
         if (!mm_wait(&full_t[at.slot], at.phase, flags)) break;
         tc_fence_after();
         const uint32_t st = smem_u32(ring + at.slot * G::kStage);
-        const uint32_t sfa = smem_u32(scales + (piece & 1) * G::kScales) + 512 * u * F::kAtoms, sfb = sfa + 4096;
+        const uint32_t sfa = smem_u32(scales + piece.slot * G::kScales) + 512 * u * F::kAtoms, sfb = sfa + 4096;
 #pragma unroll
         for (int j = 0; j < F::kAtoms; ++j) {
           tc_copy_scales<1>(tmem + G::kSfACol + 4 * j, tc_desc_scales(sfa + 512 * j));
@@ -436,7 +453,10 @@ __global__ void __launch_bounds__(kMmThreads, 2)
           tc_mma<FMT, 1>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(128, BN, F::byte(k)), tmem + G::kSfACol + 4 * F::atom(k),
                          tmem + G::kSfBCol + 4 * F::atom(k), it > 0 || k > 0);
         tc_commit<1>(&empty[at.slot]);
-        if (u == F::kPiece - 1) tc_commit<1>(&empty_s[piece++ & 1]);
+        if (u == F::kPiece - 1) {
+          tc_commit<1>(&empty_s[piece.slot]);
+          piece.next();
+        }
         at.next(l.stages);
       }
       if (it == n) {
@@ -449,7 +469,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   } else {
     const bool of_w = (warp & 1) == 0;
     ScaleTurn t{(warp - 2) >> 1};
-    scale_warp<false>(of_w ? l.unit_w : l.unit_x, t, F::kPiece, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
+    scale_warp<false, kScaleSlots>(of_w ? l.unit_w : l.unit_x, t, F::kPiece, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
                       p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, flags, 0u);
   }
   __syncwarp();
@@ -538,8 +558,11 @@ struct PairGeo {
   static constexpr int kA = 128 * 128, kB = 128 * 128;
   static constexpr int kStage = kA + kB;
   static constexpr int kScales = 3 * 4096;  // a slot of the piece ring: 32 bytes of 128 tokens and 256 features
-  static constexpr int kTurn = kPairEpilogue * 32 * 33 * 4;  // a padded 32 x 32 block per epilogue warp
-  static constexpr int kSmem = kPairStages * kStage + 2 * kScales + kTurn + 1024;
+  static constexpr int kSlots = F::kPiece == 2 ? 3 : 2;
+  static constexpr int kRows = kSlots == 3 ? 16 : 32;  // that a warp stores at a time: 32 where they fit (MXFP4 256 x 4096 x 4096: 9.9 us, 10.2 with 16)
+  static constexpr int kTurnWarp = kRows == 32 ? 32 * 32 * 4 : 32 * 17 * 4;  // a padded block of 32 x 16 words fits too
+  static constexpr int kTurn = kPairEpilogue * kTurnWarp;
+  static constexpr int kSmem = kPairStages * kStage + kSlots * kScales + kTurn + 1024;
   static constexpr int kScaleCols = 16 + 32;  // tensor-memory columns of one set of scales; two sets take turns
 };
 
@@ -567,11 +590,11 @@ __device__ __forceinline__ void pair_tile(const PairLaunch& l, unsigned i, int64
 // its 32 words (16-bit outputs: two columns a word), through the warp's block of
 // shared memory, so that lanes write neighbouring columns.  Rows of Y that start
 // at multiples of 16 bytes: 16-byte chunks of a row at places that depend on the
-// row (conflict-free both ways), whole 128-byte lines of 4 rows an instruction.
-// Others: 32 columns at a time in a padded block, an output a lane.  (An aligned
-// word a lane, shifted into place, took longer: 15.9 us against 13.2 for 1000 x
+// row (conflict-free both ways), ROWS at a time, whole 128-byte lines of 4 rows an
+// instruction.  Others: half of the columns at a time in a padded block, an
+// output a lane.  (An aligned word a lane, shifted into place, took longer: 15.9 us against 13.2 for 1000 x
 // 1001 x 1056 NVFP4.)
-template <bool OUT32>
+template <bool OUT32, int ROWS>
 __device__ __forceinline__ void store_rows(const MatmulProblem& p, uint4* stage, const uint32_t* v, int64_t t, int64_t n,
                                            bool rows16) {
   constexpr int ES = OUT32 ? 4 : 2, COLS = 128 / ES;
@@ -580,35 +603,41 @@ __device__ __forceinline__ void store_rows(const MatmulProblem& p, uint4* stage,
   unsigned char* y = reinterpret_cast<unsigned char*>(p.y) + (t * p.N + n) * ES;
   const int64_t pitch = p.N * ES;
   if (rows16) {  // the row's end is a multiple of 16 bytes too
-    __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      stage[lane * 8 + (c ^ (lane & 7))] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-    __syncwarp();
-    const int c = lane & 7;
+    for (int r0 = 0; r0 < 32; r0 += ROWS) {
+      __syncwarp();
+      if (ROWS == 32 || lane / ROWS == r0 / ROWS) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (r < rows && c * 16 < cols * ES)
-        *reinterpret_cast<uint4*>(y + r * pitch + c * 16) = stage[r * 8 + (c ^ (r & 7))];
+        for (int c = 0; c < 8; ++c)
+          stage[(lane & (ROWS - 1)) * 8 + (c ^ (lane & 7))] = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+      }
+      __syncwarp();
+      const int c = lane & 7;
+#pragma unroll
+      for (int i = 0; i < ROWS / 4; ++i) {
+        const int r = 4 * i + (lane >> 3);
+        if (r0 + r < rows && c * 16 < cols * ES)
+          *reinterpret_cast<uint4*>(y + (r0 + r) * pitch + c * 16) = stage[r * 8 + (c ^ (r & 7))];
+      }
     }
-  } else {
-    uint32_t* b = reinterpret_cast<uint32_t*>(stage);
+    return;
+  }
+  uint32_t* b = reinterpret_cast<uint32_t*>(stage);
 #pragma unroll
-    for (int k = 0; k < COLS / 32; ++k) {
-      __syncwarp();
+  for (int half = 0; half < 2; ++half) {
+    __syncwarp();
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        b[lane * 33 + c] = OUT32 ? v[c] : ((c & 1) ? v[16 * k + c / 2] >> 16 : v[16 * k + c / 2] & 0xFFFFu);
-      __syncwarp();
-      const int c = 32 * k + lane;
-      if (c < cols)
-        for (int r = 0; r < rows; ++r) {
-          if (OUT32)
-            *reinterpret_cast<uint32_t*>(y + r * pitch + c * 4) = b[r * 33 + lane];
-          else
-            *reinterpret_cast<uint16_t*>(y + r * pitch + c * 2) = (uint16_t)b[r * 33 + lane];
-        }
+    for (int c = 0; c < 16; ++c) b[lane * 17 + c] = v[16 * half + c];
+    __syncwarp();
+    if (OUT32) {
+      const int c = lane & 15, col = 16 * half + c;
+      if (col < cols)
+        for (int r = lane >> 4; r < rows; r += 2) *reinterpret_cast<uint32_t*>(y + r * pitch + col * 4) = b[r * 17 + c];
+    } else {
+      const int col = 32 * half + lane;
+      if (col < cols)
+        for (int r = 0; r < rows; ++r)
+          *reinterpret_cast<uint16_t*>(y + r * pitch + col * 2) = reinterpret_cast<const uint16_t*>(b + r * 17)[lane];
     }
   }
 }
@@ -634,7 +663,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using G = PairGeo<FMT>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
-  __shared__ uint64_t full_t[kPairStages], empty[kPairStages], full_s[2], empty_s[2], acc_full, acc_empty,
+  __shared__ uint64_t full_t[kPairStages], empty[kPairStages], full_s[G::kSlots], empty_s[G::kSlots], acc_full, acc_empty,
       given_up;
   __shared__ uint32_t tmem_base;
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
@@ -652,7 +681,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&full_t[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < G::kSlots; ++i) {
       mbar_init(&full_s[i], 2 * 3);
       mbar_init(&empty_s[i], 1);
     }
@@ -703,18 +732,19 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 9) {
     if (rank == 0 && elect_one()) {
-      unsigned turn = 0, set = 0, piece = 0;
+      unsigned turn = 0, set = 0;
+      ScaleSlot<G::kSlots> piece;
       bool ok = true;
       for (unsigned i = l.first + pair; i < l.end && ok; i += pairs, turn ^= 1) {
         if (!(ok = mm_wait(&acc_empty, turn ^ 1, flags))) break;
         tc_fence_after();
         for (int kt = k0; kt < k1; ++kt, set ^= 1) {
           const int u = kt % F::kPiece;
-          if ((u == 0 || kt == k0) && !(ok = mm_wait(&full_s[piece & 1], (piece >> 1) & 1, flags))) break;
+          if ((u == 0 || kt == k0) && !(ok = mm_wait(&full_s[piece.slot], piece.phase, flags))) break;
           if (!(ok = mm_wait(&full_t[at.slot], at.phase, flags))) break;
           tc_fence_after();
           const uint32_t st = smem_u32(ring + at.slot * G::kStage);
-          const uint32_t sa = smem_u32(scales + (piece & 1) * G::kScales) + 512 * u * F::kAtoms;
+          const uint32_t sa = smem_u32(scales + piece.slot * G::kScales) + 512 * u * F::kAtoms;
           const uint32_t sb = sa + 4096 + 512 * u * F::kAtoms;  // features' words: two blocks a scale word
           const uint32_t ca = tmem + 256 + set * G::kScaleCols, cb = ca + 16;
 #pragma unroll
@@ -729,7 +759,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc_mma<FMT, 2>(tmem, da + 2 * k, db + 2 * k, tc_idesc<FMT>(256, 256, F::byte(k)), ca + 4 * F::atom(k),
                            cb + 8 * F::atom(k), kt > k0 || k > 0);
           tc_commit<2>(&empty[at.slot], leader);
-          if (u == F::kPiece - 1 || kt == k1 - 1) tc_commit<2>(&empty_s[piece++ & 1], leader);
+          if (u == F::kPiece - 1 || kt == k1 - 1) {
+            tc_commit<2>(&empty_s[piece.slot], leader);
+            piece.next();
+          }
           at.next(kPairStages);
         }
         if (ok) tc_commit<2>(&acc_full, leader);
@@ -747,7 +780,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (unsigned i = l.first + pair; i < l.end && ok; i += pairs) {
       int64_t m, n;
       pair_tile(l, i, m, n);
-      ok = scale_warp<true>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
+      ok = scale_warp<true, G::kSlots>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
                             of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, k0, k1 - k0,
                             scales + (of_x ? 0 : 4096 + (block - 1) * 512), G::kScales, of_x ? 512 : 1024, full_s, empty_s,
                             flags, leader);
@@ -756,7 +789,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     float f1, f2_;
     tensor_factors(p, f1, f2_);
     const int q = warp & 3, half = warp >> 2;
-    uint4* stage = reinterpret_cast<uint4*>(scales + 2 * G::kScales) + warp * (32 * 33 / 4);
+    uint4* stage = reinterpret_cast<uint4*>(scales + G::kSlots * G::kScales) + warp * (G::kTurnWarp / 16);
     unsigned turn = 0;
     for (unsigned i = l.first + pair; i < l.end; i += pairs, turn ^= 1) {
       int64_t m, n;
@@ -808,7 +841,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) store_rows<false>(p, stage, o + 32 * c, t0, nn + 64 * c, l.rows16);
+        for (int c = 0; c < 2; ++c) store_rows<false, G::kRows>(p, stage, o + 32 * c, t0, nn + 64 * c, l.rows16);
       } else {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -822,7 +855,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f1 * f2_);
-          store_rows<true>(p, stage, v, t0, nn + 32 * c, l.rows16);
+          store_rows<true, G::kRows>(p, stage, v, t0, nn + 32 * c, l.rows16);
         }
       }
     }
@@ -913,7 +946,7 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
     ++l.split;
   const int64_t per = (nk + l.split - 1) / l.split;
   // one CTA an SM takes all shared memory, more tiles share an SM by three
-  const int room = ((tiles * l.split <= sms ? 220 : 74) * 1024 - 2 * G::kScales - 1024) / G::kStage;
+  const int room = ((tiles * l.split <= sms ? 220 : 74) * 1024 - kScaleSlots * G::kScales - 1024) / G::kStage;
   l.stages = (int)(per < room ? per : room);
   if (l.stages > kMmMaxStages) l.stages = kMmMaxStages;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
@@ -922,7 +955,7 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   // where an SM takes several CTAs, those of the next grid would take the places of this one unevenly
   l.early = tiles * l.split <= sms;
   // the partial tile shares the ring's memory
-  int smem = l.stages * G::kStage + 2 * G::kScales;
+  int smem = l.stages * G::kStage + kScaleSlots * G::kScales;
   if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
   smem += 1024;
   auto kern = k_matmul_tc<FMT, BN>;
