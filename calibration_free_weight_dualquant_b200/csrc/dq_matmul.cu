@@ -104,7 +104,10 @@ __device__ __forceinline__ float code_value(const unsigned char* q, int64_t at) 
 // products (exact: 16 products of at most 18 significant bits) is multiplied
 // by the two block scales at once; powers of two add their exponents, so that
 // scales at the ends of their range do not overflow on the way.  Bound by
-// fp32 arithmetic and the decoding.
+// fp32 arithmetic and the decoding: 200 x 400 x 400 NVFP4 86 us (0.7 TFLOP/s).
+// Taken only where the copies of the tensor-core kernels cannot read the codes:
+// rows of codes that do not start at multiples of 16 bytes (a 4-bit row length that
+// is not a multiple of 32, or such an address).
 template <int FMT>
 __global__ void __launch_bounds__(256) k_matmul_any(MatmulProblem p) {
   constexpr int G = FMT == FMT_NVFP4 ? 16 : 32;
@@ -183,6 +186,11 @@ static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
 // split over the CTAs of a cluster, whose partial tiles are joined through
 // distributed shared memory in rank order (no atomics: equal calls give equal
 // bits).
+//
+// Up to 64 tokens: the weight's bytes bound it, and below some 30 MB the fixed 4 us
+// of a tile's start, join and store.  1 token (GPU time): NVFP4 28672 x 4096
+// 17.3 us = 3.8 TB/s, 4096 x 4096 5.6 us (1.7 TB/s); MXFP8 4096 x 14336 13.6 us =
+// 4.5 TB/s.  16 tokens MXFP4 4096 x 14336: 9.4 us = 3.4 TB/s.
 //
 // Warps: 0 issues the copies, 1 the tensor-core work; 2 and 4 bring the
 // weights' scales, 3 and 5 the tokens', and the four write the tile out (warp w
@@ -545,9 +553,15 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 //
 // Warps: 0 .. 7 write tiles out (lane quarter w % 4, column half w / 4), 8
 // issues the copies, 9 the tensor-core work, 10 and 11 bring the tokens' scales,
-// 12 .. 15 the features' (two warps a 128-row block).  A finished tile is read into registers, rounded to
-// the output type and released before it is stored, so the next tile's
-// multiply-adds wait for the tensor-memory reads alone.
+// 12 .. 15 the features' (two warps a 128-row block).  A finished tile is read
+// into registers, rounded to the output type and released before it is stored,
+// so the next tile's multiply-adds wait for the tensor-memory reads alone.
+//
+// MXFP8 is bound by the tensor cores (the pipe is active 89 % of the time) and the
+// last wave: 4096 x 4096 x 14336 180 us = 2.7 PFLOP/s.  NVFP4 and MXFP4 do the
+// multiply-adds of the same bytes in half the time and are bound by what feeds
+// them: operands from L2 (9 TB/s) and the scales.  NVFP4 8192 x 14336 x 4096 215 us =
+// 4.5 PFLOP/s, MXFP4 8192 x 4096 x 4096 56 us = 4.9 PFLOP/s.
 constexpr int kPairThreads = 16 * 32;
 constexpr int kPairEpilogue = 8;  // warps
 constexpr int kPairStages = 5;
@@ -559,7 +573,8 @@ struct PairGeo {
   static constexpr int kStage = kA + kB;
   static constexpr int kScales = 3 * 4096;  // a slot of the piece ring: 32 bytes of 128 tokens and 256 features
   static constexpr int kSlots = F::kPiece == 2 ? 3 : 2;
-  static constexpr int kRows = kSlots == 3 ? 16 : 32;  // that a warp stores at a time: 32 where they fit (MXFP4 256 x 4096 x 4096: 9.9 us, 10.2 with 16)
+  // Rows that a warp stores at a time: 32 where they fit (MXFP4 256 x 4096 x 4096: 9.9 us, 10.2 with 16).
+  static constexpr int kRows = kSlots == 3 ? 16 : 32;
   static constexpr int kTurnWarp = kRows == 32 ? 32 * 32 * 4 : 32 * 17 * 4;  // a padded block of 32 x 16 words fits too
   static constexpr int kTurn = kPairEpilogue * kTurnWarp;
   static constexpr int kSmem = kPairStages * kStage + kSlots * kScales + kTurn + 1024;

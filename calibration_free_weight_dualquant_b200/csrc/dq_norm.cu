@@ -495,6 +495,13 @@ __device__ __forceinline__ unsigned long long amax_finish(const RowProblem& p, A
   return *reinterpret_cast<volatile unsigned long long*>(&p.hdr->amax_scaled);
 }
 
+// A CTA takes one row at a time, NC chunks of 16 elements a thread in registers
+// between the sum of squares and the quantization (NC 0: rows of more than 2048
+// chunks, read twice).  The sum is in fp64: x' has to be known to 2^-20 and
+// decided exactly where that is not enough, and one fp64 add an element is 7 % of
+// that pipe.  8192 x 4096 MXFP8 with residual: 50 us, 4.7 TB/s of the 7 bytes an
+// element; 1 x 4096: 3.8 us.  Bound by the latency of a row's loads and its two
+// barriers, with the issue slots half used.
 __host__ __device__ constexpr int norm_threads(int nc) { return nc == 1 || nc == 4 ? 512 : 256; }
 
 template <int FMT, int XDT, int NC>
@@ -727,6 +734,12 @@ __device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const G
   }
 }
 
+// A warp takes 512 columns of a row at a time, two such items in turn, so that one's
+// loads are under way while the other is computed.  8192 x 14336 MXFP8: 114 us, 5.2
+// TB/s of the 5 bytes an element; 16 x 14336: 4.7 us.  Bound by instructions (22 an
+// element: the sigmoid's exponential and reciprocal, two conversions of the
+// bracket's ends); a ring of asynchronous copies added to them: 168 us against the
+// 133 of its time.
 template <int FMT, int XDT, bool BSAME>
 __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowProblem p) {
   const int lane = threadIdx.x & 31;

@@ -12,6 +12,9 @@
  * codes fixed, projection onto representable inverse scales, requantization
  * after each update, scale 1 for an all-zero code slice) and by the DualQuant
  * (arXiv 2610.13767) summary (§3 formats, §4.3 BCD, App. B closed forms).
+ * It also runs the linear layer that such weights are for: dq_matmul multiplies
+ * them by quantized activations, which dq_act_quant, dq_norm_quant and
+ * dq_glu_quant make.
  *
  * Conventions shared by every entry point
  *  - All tensor pointers are DEVICE pointers unless the name says host; the
