@@ -384,6 +384,8 @@ def _call(device: torch.device, stream, f, *args):
     """f(stream pointer, ...) with the device of the call's tensors as the current one, and ``stream`` (default:
     that device's current stream) as the stream that new outputs and workspaces belong to."""
     index = device.index
+    if stream is not None and stream.device_index != index:
+        raise DQError(1, "a stream of the tensors' device is needed")
     if stream is None and torch._C._cuda_getDevice() == index:
         return f(torch._C._cuda_getCurrentRawStream(index), *args)
     with torch.cuda.device(device):

@@ -100,6 +100,15 @@ def test_binding_refuses_cpu_tensors_and_other_formats(lib):
         binding.dq_glu_quant(torch.zeros(2, 128, dtype=torch.bfloat16), None, "mxfp8")
 
 
+def test_binding_refuses_another_devices_stream():
+    class Stream:
+        device_index, cuda_stream = 1, 0
+
+    with pytest.raises(binding.DQError) as e:
+        binding._call(torch.device("cuda", 0), Stream(), lambda *a: None)
+    assert e.value.status == 1
+
+
 def test_reference_quantizer_pins():
     """The tests' own definition on values whose answers are known."""
     x = np.zeros((1, 32))
