@@ -197,6 +197,7 @@ static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
 // reads tensor-memory lanes 32 (w % 4) ..).
 constexpr int kMmThreads = 192;
 constexpr int kMmMaxStages = 8;
+constexpr int kMmSmem = 220 * 1024;  // most of a CTA
 
 template <int FMT, int BN>
 struct MmGeo {
@@ -220,6 +221,8 @@ struct MmGeo {
 template <int U>
 __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t piece,
                                             uint32_t (*w)[8]) {
+  unsigned here;  // keeps the loads, free among themselves, behind the wait for the grid before
+  asm volatile("mov.u32 %0, 0;" : "=r"(here)::"memory");
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int64_t r = row0 + (threadIdx.x & 31) + 32 * q;
@@ -229,23 +232,23 @@ __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0
     for (int j = 0; j < 8; ++j) w[q][j] = 0;
     if constexpr (U == 32) {
       if (left > 0)
-        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
             : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3]), "=r"(w[q][4]), "=r"(w[q][5]), "=r"(w[q][6]),
               "=r"(w[q][7])
-            : "l"(p));
+            : "l"(p), "r"(here));
     } else if constexpr (U == 16) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (16 * i < left) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          const uint4 v = reinterpret_cast<const uint4*>(p)[i];
           w[q][4 * i] = v.x, w[q][4 * i + 1] = v.y, w[q][4 * i + 2] = v.z, w[q][4 * i + 3] = v.w;
         }
     } else if (left > 0) {
       const unsigned sh = (unsigned)(uintptr_t)p & 15u;
       const unsigned char* a = p - sh;
       if (a >= s && a + 48 <= s + rows * nb) {
-        const uint4 v0 = __ldg(reinterpret_cast<const uint4*>(a)), v1 = __ldg(reinterpret_cast<const uint4*>(a) + 1),
-                    v2 = __ldg(reinterpret_cast<const uint4*>(a) + 2);
+        const uint4* a4 = reinterpret_cast<const uint4*>(a);
+        const uint4 v0 = a4[0], v1 = a4[1], v2 = a4[2];
         uint32_t t[12] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w, v2.x, v2.y, v2.z, v2.w};
 #pragma unroll
         for (int j = 0; j < 10; ++j) t[j] = sh & 8u ? t[j + 2] : t[j];
@@ -961,7 +964,7 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
     ++l.split;
   const int64_t per = (nk + l.split - 1) / l.split;
   // one CTA an SM takes all shared memory, more tiles share an SM by three
-  const int room = ((tiles * l.split <= sms ? 220 : 74) * 1024 - kScaleSlots * G::kScales - 1024) / G::kStage;
+  const int room = ((tiles * l.split <= sms ? kMmSmem : 74 * 1024) - kScaleSlots * G::kScales - 1024) / G::kStage;
   l.stages = (int)(per < room ? per : room);
   if (l.stages > kMmMaxStages) l.stages = kMmMaxStages;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
@@ -983,7 +986,8 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   // memory that is held by CTAs which wait for their own cluster.
   const int share = 228 * 1024 / 512 * G::kAlloc - 1024 - (int)fa.sharedSizeBytes;
   if (smem < share) smem = share;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the same limit in every call: another thread's call may come between this and the launch
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem);
   if (e != cudaSuccess) return e;
   return launch_early(kern, (unsigned)(tiles * l.split), kMmThreads, (size_t)smem, l.split, st, p, l, wmap, xmap);
 }

@@ -34,6 +34,7 @@ namespace dq {
 
 constexpr int kGluThreads = 256;   // dq_glu_quant's block; two an SM
 constexpr int kGluMax = 512;       // ... its largest, in a call that one cluster takes
+constexpr int kNormSmem = 4 * 512 * 64;  // g b of 4 chunks of 512 threads
 constexpr float kFltMax = 3.402823466e38f;
 
 struct RowProblem {
@@ -82,8 +83,16 @@ __device__ __forceinline__ V16 zero16() {
   for (int i = 0; i < 8; ++i) v.u[i] = 0;
   return v;
 }
+// An offset that no load can use before this point, which comes after the kernel's wait for
+// the grid before.
+__device__ __forceinline__ int64_t after_wait(int64_t off) {
+  asm volatile("" : "+l"(off)::"memory");
+  return off;
+}
+
 // An input of the call, read once: free to move above stores (a store of h to
-// the input's own place depends on the value loaded from it).
+// the input's own place depends on the value loaded from it), but not above the
+// wait for the grid before: `off` comes out of after_wait.
 __device__ __forceinline__ V16 load16(const void* base, int64_t off, bool wide) {
   const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + off;
   V16 v;
@@ -93,7 +102,8 @@ __device__ __forceinline__ V16 load16(const void* base, int64_t off, bool wide) 
         : "l"(p));
   } else {
     asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.u[0]), "=r"(v.u[1]), "=r"(v.u[2]), "=r"(v.u[3]) : "l"(p));
-    asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.u[4]), "=r"(v.u[5]), "=r"(v.u[6]), "=r"(v.u[7]) : "l"(p + 8));
+    asm("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.u[4]), "=r"(v.u[5]), "=r"(v.u[6]), "=r"(v.u[7])
+        : "l"(p + 8));
   }
   return v;
 }
@@ -140,12 +150,10 @@ __device__ __forceinline__ void pairs16(const V16& v, f2* x) {
 // The 16 column scales at col (1 where there are none).
 __device__ __forceinline__ void b16_values(const RowProblem& p, int64_t col, f2* b) {
   if (p.b_vec) {
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.b_store) + col);
-    const uint4 v0 = __ldg(q), v1 = __ldg(q + 1);
-    const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    const V16 s = load16(p.b_store, after_wait(col), false);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 f = h2_values(u[i], p.col_dt);
+      const float2 f = h2_values(s.u[i], p.col_dt);
       b[i] = pk(f.x, f.y);
     }
   } else {
@@ -383,9 +391,7 @@ __device__ __forceinline__ void gb16(const RowProblem& p, int64_t col, f2* gb) {
   b16_values(p, col, gb);
   if (p.g) {
     f2 g[8];
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.g) + col);
-    const uint4 v0 = __ldg(q), v1 = __ldg(q + 1);
-    pairs16<XDT>(V16{{v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w}}, g);
+    pairs16<XDT>(load16(p.g, after_wait(col), false), g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) gb[i] = mul2(gb[i], g[i]);  // exact: at most 22 significant bits
   }
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 2 ? 3 : 1) k_norm(cons
       isT = __frcp_rn(sT);
       sT_ok = in_range(isT);
     }
-    int64_t row0 = blockIdx.x * p.K + tid * 16;  // element of the thread's first chunk
+    int64_t row0 = after_wait(blockIdx.x * p.K + tid * 16);  // element of the thread's first chunk
 #pragma unroll 1
     for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, row0 += gridDim.x * p.K) {
       if (FMT != FMT_NVFP4 || pass == 0) {
@@ -770,7 +776,7 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
     }
     int64_t row = w0 < nw ? w0 / spans : p.M;
     int span = (int)(w0 - row * spans);
-    int64_t in = row * p.ld + (int64_t)span * 512 + lane * 16, at = row * p.K + (int64_t)span * 512 + lane * 16;
+    int64_t in = after_wait(row * p.ld + (int64_t)span * 512 + lane * 16), at = row * p.K + (int64_t)span * 512 + lane * 16;
     auto read = [&](V16& g, V16& u) {
       if (row < p.M && (int64_t)span * 512 + lane * 16 < p.K) {
         g = load16(p.x, in, p.wide);
@@ -830,8 +836,9 @@ __global__ void __launch_bounds__(kGluMax, 1) k_glu(const __grid_constant__ RowP
 static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, bool coop, int64_t want, int threads,
                               size_t smem, int sms, cudaStream_t st) {
   cudaError_t e;
+  // the same limit in every call: another thread's call may come between this and the launch
   if (smem > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+      (e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormSmem)) != cudaSuccess)
     return e;
   int grid = (int)(want < sms ? want : sms);
   if (coop && grid > 1 && grid <= 8) {  // the CTAs of a cluster need no cooperative launch and no clearing

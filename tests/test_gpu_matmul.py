@@ -7,6 +7,8 @@ infinity half a step further on, from m (1 + eps/4) at the latest: 65520 for f16
 """
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -307,3 +309,26 @@ def test_matmul_on_two_streams_at_once():
     for i in range(2):
         for y in ys[i]:
             check(y, *cases[i], "mxfp4")
+
+
+def test_matmul_from_two_threads():
+    """Calls of one kernel that take different amounts of shared memory, launched by two threads at once."""
+    cases = [[ref.to(q, "cuda") for q in case(*size, "mxfp8", 51)] for size in ((1, 512, 16384), (1, 128 * 300, 128))]
+    want = [binding.dq_matmul(x, w, "mxfp8") for x, w in cases]
+    wrong = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            ys = [binding.dq_matmul(*cases[i], "mxfp8", check=False, stream=stream) for _ in range(400)]
+            stream.synchronize()
+            wrong.extend(k for k, y in enumerate(ys) if not torch.equal(y, want[i]))
+        except Exception as e:  # reported by the test's thread
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[:3]
