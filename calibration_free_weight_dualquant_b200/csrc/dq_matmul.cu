@@ -215,59 +215,89 @@ struct MmGeo {
 // Block scales of a lane's four rows (row0 + lane + 32 q): the 32-byte piece
 // `piece` of each row, one memory sector where rows are aligned, as words
 // w[q][0 .. 7]; zeros past the matrix.  U: what the address and the length of
-// every row are multiples of, 32, 16 or (1) nothing.  With 1, three aligned
-// 16-byte reads are shifted into place; pieces whose aligned window leaves the
-// scales' memory are read by bytes.
+// every row are multiples of, 32, 16, 8 or (1) nothing.  With 1, three aligned
+// 16-byte reads are shifted into place, and pieces whose aligned window leaves the
+// scales' memory are read by bytes afterwards.  All reads of the four rows are
+// under way before the first is used.
 template <int U>
 __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0, int64_t rows, int64_t nb, int64_t piece,
                                             uint32_t (*w)[8]) {
   unsigned here;  // keeps the loads, free among themselves, behind the wait for the grid before
   asm volatile("mov.u32 %0, 0;" : "=r"(here)::"memory");
+  if constexpr (U > 1) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t r = row0 + (threadIdx.x & 31) + 32 * q;
-    const unsigned char* p = s + r * nb + piece * 32;
-    const int64_t left = r < rows ? nb - piece * 32 : 0;
+    for (int q = 0; q < 4; ++q) {
+      const int64_t r = row0 + (threadIdx.x & 31) + 32 * q;
+      const unsigned char* p = s + r * nb + piece * 32;
+      const int64_t left = r < rows ? nb - piece * 32 : 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[q][j] = 0;
-    if constexpr (U == 32) {
-      if (left > 0)
-        asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-            : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3]), "=r"(w[q][4]), "=r"(w[q][5]), "=r"(w[q][6]),
-              "=r"(w[q][7])
-            : "l"(p), "r"(here));
-    } else if constexpr (U == 16) {
+      for (int j = 0; j < 8; ++j) w[q][j] = 0;
+      if constexpr (U == 32) {
+        if (left > 0)
+          asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+              : "=r"(w[q][0]), "=r"(w[q][1]), "=r"(w[q][2]), "=r"(w[q][3]), "=r"(w[q][4]), "=r"(w[q][5]), "=r"(w[q][6]),
+                "=r"(w[q][7])
+              : "l"(p), "r"(here));
+      } else if constexpr (U == 16) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (16 * i < left) {
-          const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-          w[q][4 * i] = v.x, w[q][4 * i + 1] = v.y, w[q][4 * i + 2] = v.z, w[q][4 * i + 3] = v.w;
-        }
-    } else if (left > 0) {
-      const unsigned sh = (unsigned)(uintptr_t)p & 15u;
-      const unsigned char* a = p - sh;
-      if (a >= s && a + 48 <= s + rows * nb) {
-        const uint4* a4 = reinterpret_cast<const uint4*>(a);
-        const uint4 v0 = a4[0], v1 = a4[1], v2 = a4[2];
-        uint32_t t[12] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w, v2.x, v2.y, v2.z, v2.w};
-#pragma unroll
-        for (int j = 0; j < 10; ++j) t[j] = sh & 8u ? t[j + 2] : t[j];
-#pragma unroll
-        for (int j = 0; j < 9; ++j) t[j] = sh & 4u ? t[j + 1] : t[j];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t have = left - 4 * j;  // bytes of this word that belong to the row
-          const uint32_t v = __funnelshift_r(t[j], t[j + 1], 8 * (sh & 3u));
-          w[q][j] = have >= 4 ? v : (have > 0 ? v & (0xFFFFFFFFu >> (32 - 8 * (int)have)) : 0u);
-        }
+        for (int i = 0; i < 2; ++i)
+          if (16 * i < left) {
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+            w[q][4 * i] = v.x, w[q][4 * i + 1] = v.y, w[q][4 * i + 2] = v.z, w[q][4 * i + 3] = v.w;
+          }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t v = 0;
-#pragma unroll 1
-          for (int i = 0; i < 4; ++i)
-            if (4 * j + i < left) v |= (uint32_t)p[4 * j + i] << (8 * i);
-          w[q][j] = v;
+        for (int i = 0; i < 4; ++i)
+          if (8 * i < left) {
+            const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+            w[q][2 * i] = v.x, w[q][2 * i + 1] = v.y;
+          }
+      }
+    }
+  } else {
+    uint4 v[4][3];
+    const int64_t r0 = row0 + (threadIdx.x & 31);
+    const unsigned char* const p0 = s + r0 * nb + piece * 32;
+    const unsigned char* const end = s + rows * nb;
+    const int have = (int)min((int64_t)32, nb - piece * 32);  // bytes of the piece that belong to a row
+    bool bytes = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const unsigned char* p = p0 + 32 * q * nb;
+      const unsigned char* a = p - ((uintptr_t)p & 15u);
+      const bool on = r0 + 32 * q < rows, in = on && a >= s && a + 48 <= end;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) v[q][i] = in ? reinterpret_cast<const uint4*>(a)[i] : make_uint4(0, 0, 0, 0);
+      bytes |= on && !in;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const unsigned sh = (unsigned)(uintptr_t)(p0 + 32 * q * nb) & 15u;
+      uint32_t t[12];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) t[4 * i] = v[q][i].x, t[4 * i + 1] = v[q][i].y, t[4 * i + 2] = v[q][i].z, t[4 * i + 3] = v[q][i].w;
+#pragma unroll
+      for (int j = 0; j < 10; ++j) t[j] = sh & 8u ? t[j + 2] : t[j];
+#pragma unroll
+      for (int j = 0; j < 9; ++j) t[j] = sh & 4u ? t[j + 1] : t[j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int more = have - 4 * j;
+        const uint32_t x = __funnelshift_r(t[j], t[j + 1], 8 * (sh & 3u));
+        w[q][j] = more >= 4 ? x : (more > 0 ? x & (0xFFFFFFFFu >> (32 - 8 * more)) : 0u);
+      }
+    }
+    if (bytes) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const unsigned char* p = p0 + 32 * q * nb;
+        const unsigned char* a = p - ((uintptr_t)p & 15u);
+        if (r0 + 32 * q < rows && !(a >= s && a + 48 <= end)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (4 * j + i < have) w[q][j] |= (uint32_t)p[4 * j + i] << (8 * i);
         }
       }
     }
@@ -357,16 +387,17 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
   return true;
 }
 // `unit`: the largest power of two (32 at most) that divides the scales' address
-// and the row's length.
-template <bool PAIR, int SLOTS>
+// and the row's length.  WIDE kernels take units of 16 and 32, the others 8 and
+// less: with all four in one kernel its registers spilled (NVFP4 1000 x 4096 x
+// 11008: 28.5 us against 27.1).
+template <bool PAIR, int SLOTS, bool WIDE>
 __device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0,
                                            int64_t rows, int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes,
                                            int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags, uint32_t leader) {
 #define DQ_SCALE_LOOP(U) \
   scale_loop<PAIR, SLOTS, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, flags, leader)
-  if (unit == 32) return DQ_SCALE_LOOP(32);
-  if (unit == 16) return DQ_SCALE_LOOP(16);
-  return DQ_SCALE_LOOP(1);
+  if (WIDE) return unit == 32 ? DQ_SCALE_LOOP(32) : DQ_SCALE_LOOP(16);
+  return unit >= 8 ? DQ_SCALE_LOOP(8) : DQ_SCALE_LOOP(1);
 #undef DQ_SCALE_LOOP
 }
 
@@ -378,8 +409,8 @@ struct MmLaunch {
   int early;           // the next grid may begin from the start on (else from the end of the multiply-adds on)
 };
 
-template <int FMT, int BN>
-__global__ void __launch_bounds__(kMmThreads, 2)
+template <int FMT, int BN, bool WIDE>
+__global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
     k_matmul_tc(MatmulProblem p, MmLaunch l, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   using G = MmGeo<FMT, BN>;
   using F = TcFormat<FMT>;
@@ -480,7 +511,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
   } else {
     const bool of_w = (warp & 1) == 0;
     ScaleTurn t{(warp - 2) >> 1};
-    scale_warp<false, kScaleSlots>(of_w ? l.unit_w : l.unit_x, t, F::kPiece, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
+    scale_warp<false, kScaleSlots, WIDE>(of_w ? l.unit_w : l.unit_x, t, F::kPiece, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
                       p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, flags, 0u);
   }
   __syncwarp();
@@ -674,7 +705,7 @@ static __device__ __noinline__ void pair_give_up(const MatmulProblem& p, const P
   }
 }
 
-template <int FMT, bool OUT32>
+template <int FMT, bool OUT32, bool WIDE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_matmul_pair(const __grid_constant__ MatmulProblem p, const __grid_constant__ PairLaunch l, const __grid_constant__ CUtensorMap wmap,
                   const __grid_constant__ CUtensorMap xmap) {
@@ -798,7 +829,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (unsigned i = l.first + pair; i < l.end && ok; i += pairs) {
       int64_t m, n;
       pair_tile(l, i, m, n);
-      ok = scale_warp<true, G::kSlots>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
+      ok = scale_warp<true, G::kSlots, WIDE>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
                             of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, k0, k1 - k0,
                             scales + (of_x ? 0 : 4096 + (block - 1) * 512), G::kScales, of_x ? 512 : 1024, full_s, empty_s,
                             flags, leader);
@@ -958,37 +989,44 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   const int64_t tiles = (p.N + 127) / 128 * ((p.T + BN - 1) / BN);
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
   MmLaunch l;
-  l.split = 1;
-  // clusters of more than 2 CTAs leave some SMs of a GPC unused: 132 of 148 SMs can hold clusters of 4 or 6, 120 of 8
-  while (l.split < 8 && l.split < nk && tiles * (l.split + 1) <= (l.split < 2 ? sms : (l.split < 6 ? sms * 8 / 9 : sms * 4 / 5)))
-    ++l.split;
-  const int64_t per = (nk + l.split - 1) / l.split;
-  // one CTA an SM takes all shared memory, more tiles share an SM by three
-  const int room = ((tiles * l.split <= sms ? kMmSmem : 74 * 1024) - kScaleSlots * G::kScales - 1024) / G::kStage;
-  l.stages = (int)(per < room ? per : room);
-  if (l.stages > kMmMaxStages) l.stages = kMmMaxStages;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
   l.vec4 = vec4_rows(p);
-  // where an SM takes several CTAs, those of the next grid would take the places of this one unevenly
-  l.early = tiles * l.split <= sms;
-  // the partial tile shares the ring's memory
-  int smem = l.stages * G::kStage + kScaleSlots * G::kScales;
-  if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
-  smem += 1024;
-  auto kern = k_matmul_tc<FMT, BN>;
+  auto kern = l.unit_x >= 16 && l.unit_w >= 16 ? k_matmul_tc<FMT, BN, true> : k_matmul_tc<FMT, BN, false>;
   cudaFuncAttributes fa;
   cudaError_t e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
-  // A CTA takes at least its tensor memory's share of the SM's shared memory
-  // (228 KB, 1 KB of it per CTA reserved).  Then tensor memory never runs out on
-  // an SM before shared memory does, and no CTA of a cluster can wait for tensor
-  // memory that is held by CTAs which wait for their own cluster.
-  const int share = 228 * 1024 / 512 * G::kAlloc - 1024 - (int)fa.sharedSizeBytes;
-  if (smem < share) smem = share;
   // the same limit in every call: another thread's call may come between this and the launch
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem);
   if (e != cudaSuccess) return e;
+  int smem = 0;
+  // The largest split whose clusters all run at once (some SMs of a GPC are left
+  // over by clusters that do not divide it: 132 of 148 SMs hold clusters of 4 or 6,
+  // 120 of 8, 105 of 7; 40 x 2048 x 5632 MXFP4, 16 tiles: 15.2 us split in 7, 8.4 in 6).
+  for (l.split = (int)min((int64_t)8, min(nk, max((int64_t)1, sms / tiles)));; --l.split) {
+    const int64_t per = (nk + l.split - 1) / l.split;
+    // one CTA an SM takes all shared memory, more tiles share an SM by three
+    const int room = ((tiles * l.split <= sms ? kMmSmem : 74 * 1024) - kScaleSlots * G::kScales - 1024) / G::kStage;
+    l.stages = (int)min((int64_t)kMmMaxStages, min(per, (int64_t)room));
+    // the partial tile shares the ring's memory
+    smem = l.stages * G::kStage + kScaleSlots * G::kScales;
+    if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
+    smem += 1024;
+    // A CTA takes at least its tensor memory's share of the SM's shared memory
+    // (228 KB, 1 KB of it per CTA reserved).  Then tensor memory never runs out on
+    // an SM before shared memory does, and no CTA of a cluster can wait for tensor
+    // memory that is held by CTAs which wait for their own cluster.
+    smem = max(smem, 228 * 1024 / 512 * G::kAlloc - 1024 - (int)fa.sharedSizeBytes);
+    if (l.split <= 2) break;  // clusters of 2 fit everywhere
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute at;
+    cluster_config(&cfg, &at, (unsigned)(tiles * l.split), kMmThreads, (size_t)smem, l.split);
+    int clusters = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg)) != cudaSuccess) return e;
+    if (clusters >= tiles) break;
+  }
+  // where an SM takes several CTAs, those of the next grid would take the places of this one unevenly
+  l.early = tiles * l.split <= sms;
   return launch_early(kern, (unsigned)(tiles * l.split), kMmThreads, (size_t)smem, l.split, st, p, l, wmap, xmap);
 }
 
@@ -1011,7 +1049,7 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
   l.rows16 = ((uintptr_t)p.y | (uintptr_t)(p.N * (OUT32 ? 4 : 2))) % 16 == 0;
   l.vec4 = vec4_rows(p);
-  auto kern = k_matmul_pair<FMT, OUT32>;
+  auto kern = l.unit_x >= 16 && l.unit_w >= 16 ? k_matmul_pair<FMT, OUT32, true> : k_matmul_pair<FMT, OUT32, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned tiles = l.tiles_m * l.tiles_n, pairs = (unsigned)sms / 2;
