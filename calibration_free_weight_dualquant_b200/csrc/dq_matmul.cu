@@ -187,10 +187,10 @@ static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
 // distributed shared memory in rank order (no atomics: equal calls give equal
 // bits).
 //
-// Up to 64 tokens: the weight's bytes bound it, and below some 30 MB the fixed 4 us
-// of a tile's start, join and store.  1 token (GPU time): NVFP4 28672 x 4096
-// 17.3 us = 3.8 TB/s, 4096 x 4096 5.6 us (1.7 TB/s); MXFP8 4096 x 14336 13.6 us =
-// 4.5 TB/s.  16 tokens MXFP4 4096 x 14336: 9.4 us = 3.4 TB/s.
+// Up to 64 tokens: the weight's bytes bound it, and below some 30 MB the fixed 3.5
+// us of a tile's start, join and store.  1 token (GPU time): NVFP4 28672 x 4096 @
+// us, 4096 x 4096 5.2 us (1.8 TB/s); MXFP8 4096 x 14336 13.0 us = 4.7
+// TB/s.  16 tokens MXFP4 4096 x 14336: 7.9 us = 4.0 TB/s.
 //
 // Warps: 0 issues the copies, 1 the tensor-core work; 2 and 4 bring the
 // weights' scales, 3 and 5 the tokens', and the four write the tile out (warp w
@@ -450,6 +450,8 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
     tma_prefetch_map(&wmap);
     tma_prefetch_map(&xmap);
   }
+  __syncwarp();
+  if (l.split > 1) cluster_arrive();
   if (l.early) griddep_launch_dependents();
   griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && flags) *reinterpret_cast<volatile unsigned*>(flags) = 0;
@@ -518,32 +520,55 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
 
   if (!l.early) griddep_launch_dependents();
 
-  // the finished tile: tensor-memory lane = feature, column = token
+  // the finished tile: tensor-memory lane = feature, column = token.  Of a split
+  // tile every CTA sums its share of the tokens, in rank order; the others write
+  // their parts into its shared memory.  (Reading them from there cost the latency
+  // of that network once more: 1 x 4096 x 4096 MXFP8 6.2 us against 5.9.)
   const int tv = (int)min((int64_t)BN, p.T - t0);
+  const int share = (tv + l.split - 1) / l.split;
+  float* const parts = reinterpret_cast<float*>(scales + kScaleSlots * G::kScales);  // [rank][token][128 features]
   bool ok = true;
+  if (l.split > 1) cluster_wait();  // every CTA of the cluster has begun
   if (warp >= 2) {
     ok = __all_sync(0xffffffffu, mm_wait(&acc_full, 0, flags));
     tc_fence_after();
     const int q = warp & 3;
     const int64_t nn = n0 + 32 * q + lane;
-    float* part = reinterpret_cast<float*>(ring);  // [token][128 features]: the ring is idle now
+    const uint32_t mine = smem_u32(parts) + 4 * ((int)rank * share * 128 + 32 * q + lane);
+    int owner = 0, at = 0;  // of token c + i, and its place there
+    constexpr int C = BN < 32 ? BN : 32;
 #pragma unroll 1
-    for (int c = 0; c < tv; c += 16) {
-      uint32_t v[16];
-      if (ok) {
-        tc_load16(tmem + ((uint32_t)(32 * q) << 16) + c, v);
-        tc_load_wait16(v);
-      } else {  // a wait ran out: no number that looks like a result
+    for (int c = 0; c < tv; c += C) {
+      uint32_t v[C];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0x7FC00000u;
+      for (int i = 0; i < C; i += 16) tc_load16(tmem + ((uint32_t)(32 * q) << 16) + c + i, v + i);
+#pragma unroll
+      for (int i = 0; i < C; i += 16) tc_load_wait16(v + i);
+      if (!ok) {  // a wait ran out: no number that looks like a result
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = 0x7FC00000u;
       }
+      // Branches outside, predicates within: one warp a scheduler hides no branch (with them 16 tokens took 1.1 us;
+      // 64 x 4096 x 4096 NVFP4 10.3 us against 7.0).
+      if (l.split > 1) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (c + i < tv) {
-          if (l.split > 1)
-            part[(c + i) * 128 + 32 * q + lane] = __uint_as_float(v[i]);
-          else if (nn < p.N)
-            y_store(p.y, p.y_dt, (t0 + c + i) * p.N + nn, __uint_as_float(v[i]) * f1 * f2);
+        for (int i = 0; i < C; ++i) {
+          st_cluster_if(c + i < tv, mine + 512 * at, (uint32_t)owner, v[i]);
+          ++at;
+          owner += at == share;
+          at = at == share ? 0 : at;
+        }
+      } else if (p.y_dt == DT_F32) {
+        float* y = reinterpret_cast<float*>(p.y) + (t0 + c) * p.N + nn;
+#pragma unroll
+        for (int i = 0; i < C; ++i, y += p.N)
+          if (c + i < tv && nn < p.N) *y = __uint_as_float(v[i]) * f1 * f2;
+      } else {
+        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + (t0 + c) * p.N + nn;
+#pragma unroll
+        for (int i = 0; i < C; ++i, y += p.N) {
+          const uint16_t o = (uint16_t)pack16(__uint_as_float(v[i]) * f1 * f2, 0.f, p.y_dt);
+          if (c + i < tv && nn < p.N) *y = o;
         }
       }
     }
@@ -551,22 +576,18 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
   }
   if (l.split > 1) {
     cluster_sync();
-    const uint32_t part = smem_u32(ring);
-    const int total = tv * 32;  // groups of four features
-    for (int e = (int)rank * kMmThreads + threadIdx.x; e < total; e += l.split * kMmThreads) {
-      float4 v[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r < l.split) v[r] = ld_cluster_f4(part + 16 * e, r);
+    const int first = (int)rank * share, total = min(share, tv - first) * 32;  // groups of four features
+    for (int e = threadIdx.x; e < total; e += kMmThreads) {
+      const float4* v = reinterpret_cast<const float4*>(parts) + e;
       float4 s = v[0];
-#pragma unroll
-      for (int r = 1; r < 8; ++r)
-        if (r < l.split) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
-      const int64_t nn = n0 + 4 * (e & 31), at = (t0 + (e >> 5)) * p.N + nn;
+      for (int r = 1; r < l.split; ++r) {
+        const float4 o = v[r * share * 32];
+        s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+      }
+      const int64_t nn = n0 + 4 * (e & 31), at = (t0 + first + (e >> 5)) * p.N + nn;
       const float o[4] = {s.x * f1 * f2, s.y * f1 * f2, s.z * f1 * f2, s.w * f1 * f2};
       y_store4(p.y, p.y_dt, at, o, p.N - nn, l.vec4);
     }
-    cluster_sync();
   } else {
     __syncthreads();
   }
@@ -1005,13 +1026,11 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   // 120 of 8, 105 of 7; 40 x 2048 x 5632 MXFP4, 16 tiles: 15.2 us split in 7, 8.4 in 6).
   for (l.split = (int)min((int64_t)8, min(nk, max((int64_t)1, sms / tiles)));; --l.split) {
     const int64_t per = (nk + l.split - 1) / l.split;
+    const int fixed = kScaleSlots * G::kScales + 1024 + (l.split > 1 ? (BN + l.split - 1) / l.split * l.split * 512 : 0);
     // one CTA an SM takes all shared memory, more tiles share an SM by three
-    const int room = ((tiles * l.split <= sms ? kMmSmem : 74 * 1024) - kScaleSlots * G::kScales - 1024) / G::kStage;
+    const int room = ((tiles * l.split <= sms ? kMmSmem : 74 * 1024) - fixed) / G::kStage;
     l.stages = (int)min((int64_t)kMmMaxStages, min(per, (int64_t)room));
-    // the partial tile shares the ring's memory
-    smem = l.stages * G::kStage + kScaleSlots * G::kScales;
-    if (l.split > 1 && smem < BN * 128 * 4) smem = BN * 128 * 4;
-    smem += 1024;
+    smem = l.stages * G::kStage + fixed;
     // A CTA takes at least its tensor memory's share of the SM's shared memory
     // (228 KB, 1 KB of it per CTA reserved).  Then tensor memory never runs out on
     // an SM before shared memory does, and no CTA of a cluster can wait for tensor

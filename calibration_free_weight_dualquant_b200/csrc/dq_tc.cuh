@@ -192,6 +192,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of one more meeting of the cluster, before which nobody has written anything for the others.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// If `on`, a word to this CTA's shared address `addr` in the cluster's CTA `rank`.
+__device__ __forceinline__ void st_cluster_if(bool on, uint32_t addr, uint32_t rank, uint32_t v) {
+  asm volatile(
+      "{\n.reg .b32 a;\n.reg .pred p;\nsetp.ne.b32 p, %3, 0;\n@p mapa.shared::cluster.u32 a, %0, %1;\n"
+      "@p st.shared::cluster.b32 [a], %2;\n}" ::"r"(addr),
+      "r"(rank), "r"(v), "r"((int)on)
+      : "memory");
+}
 // Four fp32 values at this CTA's shared address `addr` in the cluster's CTA `rank`.
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
   uint32_t a;
