@@ -187,10 +187,12 @@ static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
 // distributed shared memory in rank order (no atomics: equal calls give equal
 // bits).
 //
-// Up to 64 tokens: the weight's bytes bound it, and below some 30 MB the fixed 3.5
-// us of a tile's start, join and store.  1 token (GPU time): NVFP4 28672 x 4096 @
-// us, 4096 x 4096 5.2 us (1.8 TB/s); MXFP8 4096 x 14336 13.0 us = 4.7
-// TB/s.  16 tokens MXFP4 4096 x 14336: 7.9 us = 4.0 TB/s.
+// Up to 64 tokens the weight's bytes bound it, and below some 30 MB the fixed 3.5
+// us of a tile's start, join and store.  1 token (GPU time): NVFP4 28672 x 4096
+// 15.4 us = 4.3 TB/s, 4096 x 4096 5.2 us (1.8 TB/s); MXFP8 4096 x 14336 13.0 us =
+// 4.7 TB/s.  16 tokens MXFP4 4096 x 14336: 7.9 us = 4.0 TB/s.  More tokens, as long
+// as the tiles are few (tc_ns): 64 or 128 a tile; 1000 x 1001 x 1056 NVFP4 7.1 us,
+// 12.1 with pairs of CTAs.
 //
 // Warps: 0 issues the copies, 1 the tensor-core work; 2 and 4 bring the
 // weights' scales, 3 and 5 the tokens', and the four write the tile out (warp w
@@ -932,7 +934,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
   __syncwarp();
   if (l.split > 1) {
-    // each CTA joins and stores its share of the 128 rows that the pairs' CTAs of its rank hold, in pair order
+    // each CTA joins and stores its share of the 128 rows, as many as there are, that the pairs' CTAs of its rank hold, in pair order
     if (__any_sync(0xffffffffu, gave_up))
       for (int e = lane; e < 32 * 128; e += 32)  // a wait ran out: no number that looks like a result
         reinterpret_cast<float*>(ring)[(32 * (warp & 3) + (e >> 7)) * kPartPitch + 128 * (warp >> 2) + (e & 127)] =
@@ -942,12 +944,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tensor_factors(p, f1, f2_);
     int64_t m, n;
     pair_tile(l, l.first + pair, m, n);
-    const int rows = (128 + l.split - 1) / l.split;
+    const int tv = (int)max((int64_t)0, min((int64_t)128, p.T - m * 256 - rank * 128)), rows = (tv + l.split - 1) / l.split;
     const uint32_t part = smem_u32(ring);
-    for (int e = threadIdx.x; e < rows * 64; e += kPairThreads) {
+    for (int e = threadIdx.x; e < min(rows, tv - share * rows) * 64; e += kPairThreads) {
       const int row = share * rows + (e >> 6), col = 4 * (e & 63);
       const int64_t t = m * 256 + rank * 128 + row, nn = n * 256 + col;
-      if (row >= 128 || t >= p.T || nn >= p.N) continue;
+      if (nn >= p.N) continue;
       float4 v[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -1101,13 +1103,38 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
   return launch_early(kern, rest * 2 * split, kPairThreads, (size_t)G::kSmem, 2 * split, st, p, l, wmap, xmap);
 }
 
+// About how long a product takes, in ns, to choose between the kernels: a fixed
+// part, with the join of split tiles, and the K tiles that a CTA works on, each the
+// time that its SM's operands take to arrive, whichever the kernel (measured: 70
+// bytes a ns with a scale per 16, 90 with one per 32).  Chosen by this, the kernel
+// was within 10 % of the fastest of the three in nearly all of 270 products of 65 to
+// 1500 tokens; the pairs for all of them took up to 1.7 times as long (192 x 4096 x
+// 1024 NVFP4: 64 tokens a tile 5.3 us, 128 8.2, pairs 6.9; 128 x 4096 x 14336: 15.9,
+// 12.9 and 16.9; 300 x 4096 x 14336: 34.4, 25.3 and 20.5).
+constexpr int tile_ns(int fmt, int bn) { return (128 + bn) * 128 / (fmt == FMT_NVFP4 ? 70 : 90); }
+static int64_t tc_ns(const MatmulProblem& p, int fmt, int64_t nk, int bn, int sms) {
+  const int64_t tiles = (p.N + 127) / 128 * ((p.T + bn - 1) / bn);
+  const int64_t split = max((int64_t)1, min((int64_t)8, min(nk, sms / tiles)));
+  return 3600 + (split > 1 ? 20 * bn : 0) + (tiles + sms - 1) / sms * ((nk + split - 1) / split) * tile_ns(fmt, bn);
+}
+static int64_t pair_ns(const MatmulProblem& p, int fmt, int64_t nk, int sms) {
+  const int64_t tiles = (p.N + 255) / 256 * ((p.T + 255) / 256), pairs = sms / 2;
+  int64_t split = 4;
+  while (split > 1 && (tiles * split > pairs || nk * (split - 1) < 12 * split)) --split;
+  return (split > 1 ? 9000 : 6000) + (tiles + pairs - 1) / pairs * ((nk + split - 1) / split) * tile_ns(fmt, 128);
+}
+
 template <int FMT>
 static cudaError_t matmul_fmt(const MatmulProblem& p, int sms, cudaStream_t st) {
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
   if (((uintptr_t)p.xq | (uintptr_t)p.wq | (uintptr_t)row_bytes) % 16 != 0) return matmul_any<FMT>(p, st);
   if (p.T <= 16) return matmul_tc<FMT, 16>(p, sms, st);
   if (p.T <= 32) return matmul_tc<FMT, 32>(p, sms, st);
-  if (p.T <= 64) return matmul_tc<FMT, 64>(p, sms, st);
+  const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
+  const int64_t t64 = tc_ns(p, FMT, nk, 64, sms), t128 = tc_ns(p, FMT, nk, 128, sms), two = pair_ns(p, FMT, nk, sms);
+  if (p.T <= 64 || (t64 <= t128 && t64 <= two)) return matmul_tc<FMT, 64>(p, sms, st);
+  // 128 tokens a tile leave no shared memory for a second CTA of an SM
+  if ((p.N + 127) / 128 * ((p.T + 127) / 128) <= sms && t128 <= two) return matmul_tc<FMT, 128>(p, sms, st);
   return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, sms, st) : matmul_pair<FMT, false>(p, sms, st);
 }
 

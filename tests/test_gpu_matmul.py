@@ -59,6 +59,9 @@ SHAPES = [
     (300, 96, 8192), (700, 1000, 1312), (1025, 2049, 160),
     # tiles of 256 x 256 left over after whole waves of the SM pairs, split in 2, 3 and 4, and a part of a wave
     (2300, 2500, 4096), (2500, 2300, 1024), (2000, 2600, 4096), (500, 2049, 4096), (300, 600, 4096),
+    # tiles of 64 and 128 tokens, whole and split, and few pairs' tiles split in 4, 3 and 2
+    (192, 4096, 1024), (130, 300, 2048), (128, 4096, 4096), (200, 2000, 12032), (180, 4090, 14336), (260, 3000, 14336),
+    (300, 4096, 14336),
 ]
 
 
