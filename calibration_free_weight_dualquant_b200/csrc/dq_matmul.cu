@@ -34,7 +34,9 @@ struct MatmulProblem {
 };
 
 // The tensor scales' product as f1 * f2, applied one after the other: f2 is 1
-// unless the product leaves fp32's normal range.
+// unless the product leaves fp32's normal range, and finite: beyond 2^255 the
+// largest number does, since the smallest nonzero sum, 2^-20, leaves the range all
+// the same and a zero sum stays zero.
 __device__ __forceinline__ void tensor_factors(const MatmulProblem& p, float& f1, float& f2) {
   f1 = f2 = 1.f;
   if (p.x_sT == nullptr) return;
@@ -45,7 +47,8 @@ __device__ __forceinline__ void tensor_factors(const MatmulProblem& p, float& f1
   } else {
     const int e = ilogb(s) < 0 ? -126 : 127;
     f1 = scalbnf(1.f, e);
-    f2 = (float)scalbn(s, -e);
+    const double top = 3.4028234663852886e38;
+    f2 = (float)fmin(fmax(scalbn(s, -e), -top), top);
   }
 }
 
