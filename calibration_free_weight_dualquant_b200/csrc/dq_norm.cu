@@ -600,7 +600,10 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 2 ? 3 : 1) k_norm(cons
         rstd = p.rstd[row];
       }
       const float rs = (float)rstd;
-      const bool rs_ok = rs >= 0x1p-100f && rs <= 0x1p100f;
+      // x' = h (rs gb): with rs from 2^-30 on a product rs gb that loses bits below fp32's normal range leaves |x'| < 2^-80
+      // (|h| rs <= sqrt(K)), a zero code in every group whose scale the fast path settles (from 2^-60 on); one beyond
+      // the range shows as an infinity or a NaN.  (h rs) gb would bring a subnormal h rs back into range.
+      const bool rs_ok = rs >= 0x1p-30f && rs <= 0x1p100f;
 #pragma unroll 1
       for (int t = 0; t < trips; ++t) {
 #pragma unroll
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(norm_threads(NC), NC == 2 ? 3 : 1) k_norm(cons
           f2 v[8];
           pairs16<XDT>(hv[c], v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = mul2(mul2(v[i], splat(rs)), gb[i]);
+          for (int i = 0; i < 8; ++i) v[i] = mul2(v[i], mul2(gb[i], splat(rs)));
           if (FMT == FMT_NVFP4 && pass == 0) {
             // values that are not finite have no share in the tensor scale
             amax_add<XDT, false>(p, amax, absmax16(v), row0 + i0 * 16, on && rstd == rstd && !zero_bits16(hv[c]), !rs_ok, rstd);

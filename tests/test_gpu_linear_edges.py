@@ -1,5 +1,5 @@
 """Ends of the ranges of the quantized linear layer's operators: tensor scales whose product leaves fp32's range
-upwards."""
+upwards, and norms of values so small that their share of the row is subnormal."""
 from __future__ import annotations
 
 import numpy as np
@@ -7,9 +7,11 @@ import pytest
 import torch
 
 import linear_ref as ref
-from calibration_free_weight_dualquant_b200 import binding
+from calibration_free_weight_dualquant_b200 import binding, synth
 
 pytestmark = pytest.mark.gpu
+
+FMTS = ["nvfp4", "mxfp4", "mxfp8"]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -33,3 +35,27 @@ def test_matmul_tensor_scales_near_the_largest(dt, tokens, rows, cols):
     want, _ = ref.matmul(x, w, "nvfp4")
     assert (want[3] == 0).all() and (want[:, 41] == 0).all()
     assert np.array_equal(ref.f64(y), np.where(want == 0, 0.0, np.copysign(np.inf, want)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("tokens,cols", [(40, 2048), (700, 1024), (3, 9216), (2, 40000)])
+def test_norm_of_tiny_values_in_large_rows(fmt, tokens, cols):
+    """h / rms(h) is subnormal in fp32 where g b brings it back into range: scales and codes are those of the fp64
+    values all the same."""
+    rng = torch.Generator().manual_seed(tokens + cols)
+    x = 1000 * synth.make_activations(tokens, cols, seed=5).float()
+    w = 1 + 0.3 * torch.randn(cols, generator=rng)
+    b = torch.ones(cols)
+    tiny = (torch.arange(cols) // ref.GROUP[fmt]) % 2 == 1
+    k = torch.randint(-7, 8, (tokens, cols), generator=rng).double() * 2.0 ** -133
+    x = torch.where(tiny, k, x.double()).to(torch.bfloat16)
+    assert (x[:, tiny].double() == k[:, tiny]).all()  # bf16 subnormals
+    w = torch.where(tiny, w.abs().clamp(0.5, 1.5) * 2.0 ** 120, w).to(torch.bfloat16)
+    b = torch.where(tiny, torch.tensor(2.0 ** 5), b).to(torch.bfloat16)
+    got = binding.dq_norm_quant(x.cuda(), w.cuda(), b.cuda(), fmt)
+    want = ref.quantize(ref.norm(x, None, w, b, 1e-5)[1], fmt)
+    if fmt == "nvfp4":
+        assert np.float32(got["tensor_scale"].cpu()[0]) == want["tensor_scale"]
+    for name in ("block_scales", "codes"):
+        bad = got[name].cpu().numpy() != want[name]
+        assert not bad.any(), "%s: %d of %d differ" % (name, bad.sum(), bad.size)
