@@ -310,11 +310,14 @@ __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0
 }
 
 // Bounded wait for a ring barrier, by the clock alone: the header's flags may
-// still hold what the workspace held before this launch.
+// still hold what the workspace held before this launch.  CLUSTER: another CTA
+// signals the barrier too.
+template <bool CLUSTER>
 __device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned* flags) {
-  if (mbar_try_wait(bar, parity)) return true;
+  auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const unsigned long long t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!done()) {
     if (global_ns() - t0 > kWaitLimitNs) {
       if (flags) atomicOr(flags, kFlagTimeout);
       return false;
@@ -375,7 +378,7 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
     uint32_t w[4][8];
     load_scales<U>(s, row0, rows, nb, piece, w);
     const unsigned use = t.piece / SLOTS, slot = t.piece - use * SLOTS;
-    if (!__all_sync(0xffffffffu, mm_wait(&empty[slot], (use & 1) ^ 1, flags))) return false;
+    if (!__all_sync(0xffffffffu, mm_wait<PAIR>(&empty[slot], (use & 1) ^ 1, flags))) return false;
     unsigned char* dst = ring + slot * slot_bytes + lane * 16;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
       unsigned phase = 1;
       bool ok = true;
       for (; issued < n; ++issued) {
-        if (!(ok = mm_wait(&empty[slot], phase, flags))) break;
+        if (!(ok = mm_wait<false>(&empty[slot], phase, flags))) break;
         unsigned char* st = ring + slot * G::kStage;
         mbar_arrive_expect_tx(&full_t[slot], G::kA + G::kB);
         tma_load_2d(st, &wmap, (int)((k0 + issued) * 128), (int)n0, &full_t[slot]);
@@ -486,8 +489,8 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
       int it = 0;
       for (; it < n; ++it) {
         const int kt = (int)k0 + it, u = kt % F::kPiece;
-        if ((it == 0 || u == 0) && !mm_wait(&full_s[piece.slot], piece.phase, flags)) break;
-        if (!mm_wait(&full_t[at.slot], at.phase, flags)) break;
+        if ((it == 0 || u == 0) && !mm_wait<false>(&full_s[piece.slot], piece.phase, flags)) break;
+        if (!mm_wait<false>(&full_t[at.slot], at.phase, flags)) break;
         tc_fence_after();
         const uint32_t st = smem_u32(ring + at.slot * G::kStage);
         const uint32_t sfa = smem_u32(scales + piece.slot * G::kScales) + 512 * u * F::kAtoms, sfb = sfa + 4096;
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
   bool ok = true;
   if (l.split > 1) cluster_wait();  // every CTA of the cluster has begun
   if (warp >= 2) {
-    ok = __all_sync(0xffffffffu, mm_wait(&acc_full, 0, flags));
+    ok = __all_sync(0xffffffffu, mm_wait<false>(&acc_full, 0, flags));
     tc_fence_after();
     const int q = warp & 3;
     const int64_t nn = n0 + 32 * q + lane;
@@ -793,7 +796,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         int64_t m, n;
         pair_tile(l, i, m, n);
         for (int kt = k0; kt < k1; ++kt, ++issued) {
-          if (!(ok = mm_wait(&empty[at.slot], at.phase ^ 1, flags))) break;
+          if (!(ok = mm_wait<true>(&empty[at.slot], at.phase ^ 1, flags))) break;
           unsigned char* st = ring + at.slot * G::kStage;
           if (rank == 0) mbar_arrive_expect_tx(&full_t[at.slot], 2 * (G::kA + G::kB));
           tma_load_2d_pair(st, &xmap, kt * 128, (int)(m * 256 + rank * 128), &full_t[at.slot]);
@@ -811,12 +814,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       ScaleSlot<G::kSlots> piece;
       bool ok = true;
       for (unsigned i = l.first + pair; i < l.end && ok; i += pairs, turn ^= 1) {
-        if (!(ok = mm_wait(&acc_empty, turn ^ 1, flags))) break;
+        if (!(ok = mm_wait<true>(&acc_empty, turn ^ 1, flags))) break;
         tc_fence_after();
         for (int kt = k0; kt < k1; ++kt, set ^= 1) {
           const int u = kt % F::kPiece;
-          if ((u == 0 || kt == k0) && !(ok = mm_wait(&full_s[piece.slot], piece.phase, flags))) break;
-          if (!(ok = mm_wait(&full_t[at.slot], at.phase, flags))) break;
+          if ((u == 0 || kt == k0) && !(ok = mm_wait<true>(&full_s[piece.slot], piece.phase, flags))) break;
+          if (!(ok = mm_wait<true>(&full_t[at.slot], at.phase, flags))) break;
           tc_fence_after();
           const uint32_t st = smem_u32(ring + at.slot * G::kStage);
           const uint32_t sa = smem_u32(scales + piece.slot * G::kScales) + 512 * u * F::kAtoms;
@@ -869,7 +872,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (unsigned i = l.first + pair; i < l.end; i += pairs, turn ^= 1) {
       int64_t m, n;
       pair_tile(l, i, m, n);
-      if (!__all_sync(0xffffffffu, mm_wait(&acc_full, turn, flags))) {
+      if (!__all_sync(0xffffffffu, mm_wait<true>(&acc_full, turn, flags))) {
         if (l.split > 1)
           gave_up = true;
         else

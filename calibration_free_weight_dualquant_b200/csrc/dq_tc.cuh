@@ -136,17 +136,30 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, int
       : "memory");
 }
 
-// Arrival on the barrier at this place in the cluster's CTA `rank`.  Release at
-// the CTA's scope: what it publishes are writes to this CTA's shared memory, read
-// by this SM's tensor core after a proxy fence, and tensor-memory reads that a
-// tcgen05 fence ordered.  At cluster scope the arrival waited for the warp's
-// memory traffic, about 1500 clocks.
+// Arrival on the barrier at this place in the cluster's CTA `rank`, released to
+// the cluster: what it publishes are writes to this CTA's shared memory, so the
+// fence is the one of that memory alone.  (A release of all memory waited for the
+// warp's global traffic, about 1500 clocks: NVFP4 8192 x 14336 x 4096 470 us
+// against 273 then.)  Waited for with mbar_try_wait_cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
   asm volatile(
       "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %0, %1;\n"
-      "mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar)),
+      "fence.release.sync_restrict::shared::cta.cluster;\n"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar)),
       "r"(rank)
       : "memory");
+}
+// mbar_try_wait on a barrier of this CTA that another CTA of the cluster arrives
+// at or copies to: acquires the cluster's shared memory.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, unsigned parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n"
+      "@p fence.acquire.sync_restrict::shared::cluster.cluster;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // 16 consecutive columns of this warp's lane quarter, one lane a thread.
