@@ -651,7 +651,6 @@ struct PairLaunch {
   int rows16;  // rows of Y start at multiples of 16 bytes
   int vec4;   // fours of outputs are aligned
   int split;  // pairs of a cluster, each with its share of the K tiles of one tile
-  int last;   // no launch over the rest of the tiles follows
 };
 constexpr int kPartPitch = 260;  // floats of a partial tile's row in shared memory: conflict-free both ways
 
@@ -774,16 +773,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  // The first launch's whole waves run before the rest's; what the call reads is
-  // complete when the first launch's wait returns, and only then may the second
-  // begin, which waits for the first at its end.
   if (warp == 8 && elect_one()) {
     tma_prefetch_map(&xmap);
     tma_prefetch_map(&wmap);
   }
-  if (l.last) griddep_launch_dependents();
-  if (l.first == 0) griddep_wait();
-  if (!l.last) griddep_launch_dependents();
+  griddep_launch_dependents();
+  griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && flags && l.first == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   MmSlot at;
   bool gave_up = false;
@@ -968,7 +963,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       y_store4(p.y, p.y_dt, t * p.N + nn, o, p.N - nn, l.vec4);
     }
   }
-  if (l.first != 0) griddep_wait();
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still signal it or read its shared memory
   if (warp == 9) {
@@ -1098,14 +1092,12 @@ static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st)
     l.first = 0;
     l.end = whole;
     l.split = 1;
-    l.last = whole == tiles;
     e = launch_early(kern, 2 * (whole < pairs ? whole : pairs), kPairThreads, (size_t)G::kSmem, 2, st, p, l, wmap, xmap);
-    if (e != cudaSuccess || l.last) return e;
+    if (e != cudaSuccess || whole == tiles) return e;
   }
   l.first = whole;
   l.end = tiles;
   l.split = split;
-  l.last = 1;
   return launch_early(kern, rest * 2 * split, kPairThreads, (size_t)G::kSmem, 2 * split, st, p, l, wmap, xmap);
 }
 
