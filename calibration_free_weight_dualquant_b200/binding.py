@@ -113,6 +113,8 @@ def load_library():
     lib.dq_act_quant.restype = I
     lib.dq_matmul.argtypes = [ctypes.POINTER(_Outputs), I64, ctypes.POINTER(_Outputs), I64, I64, I, I, P, I, P, SZ, P]
     lib.dq_matmul.restype = I
+    lib.dq_matmul_selftest.argtypes = lib.dq_matmul.argtypes[:-1] + [ctypes.c_uint, I, I, ctypes.c_uint, P]
+    lib.dq_matmul_selftest.restype = I
     lib.dq_norm_workspace_bytes.argtypes = [I64, I64, I, I]
     lib.dq_norm_workspace_bytes.restype = SZ
     lib.dq_norm_quant.argtypes = [P, P, I, I64, I64, P, ctypes.c_float, P, I, I, I, ctypes.POINTER(_Outputs), P, P, SZ,
@@ -430,6 +432,23 @@ def dq_matmul(X: dict, W: dict, fmt, group: Optional[int] = None, out: Optional[
     if dt is None:
         raise DQError(1, "dq_matmul: out_dtype must be float32, bfloat16 or float16")
     return _call(codes.device, stream, m.matmul, X, W, f, out, dt, workspace, bool(check))
+
+
+def matmul_selftest(X: dict, W: dict, fmt, out: torch.Tensor, workspace: torch.Tensor, rank: int, role: int, at: int,
+                    wait_ns: int = 2_000_000, stream=None) -> int:
+    """dq_matmul into ``out`` with one role of a CTA withheld (dq_matmul_selftest) on the current device; returns the
+    status it leaves in ``workspace``: DQ_ECUDA (5) where a wait ran out."""
+    lib = load_library()
+    f = _fmt(fmt)
+    x, w = (_Outputs(q["codes"].data_ptr(), q["block_scales"].data_ptr(),
+                     q["tensor_scale"].data_ptr() if f == Format.NVFP4 else None, None, None) for q in (X, W))
+    cols = X["codes"].shape[1] * (1 if f == Format.MXFP8 else 2)
+    st = lib.dq_matmul_selftest(ctypes.byref(x), X["codes"].shape[0], ctypes.byref(w), W["codes"].shape[0], cols, int(f),
+                                DEFAULT_GROUP[f], out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(),
+                                workspace.numel(), wait_ns, rank, role, at, _stream_ptr(stream))
+    if st != 0:
+        raise DQError(st, "dq_matmul_selftest")
+    return lib.dq_sync_status(workspace.data_ptr(), _stream_ptr(stream))
 
 
 def dq_norm_quant(X: torch.Tensor, weight: Optional[torch.Tensor], col_scales: Optional[torch.Tensor], fmt,

@@ -10,6 +10,7 @@
 
 #include <cuda.h>
 #include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
+#include <math_constants.h>
 
 #include "dq.h"
 #include "dq_device.cuh"
@@ -309,21 +310,41 @@ __device__ __forceinline__ void load_scales(const unsigned char* s, int64_t row0
   }
 }
 
+// How long waits last, and what a self-test withholds: a role of the CTA `rank` of
+// every cluster stops as if its wait had run out, after `at` K tiles (role 0, the
+// copies) or pieces of 32 bytes a row (1, the weights' scales; 2, the tokens').
+// Eight bytes, for a launch's parameters are read from memory a 64-byte line at a time.
+struct MmWait {
+  unsigned limit_ns = (unsigned)kWaitLimitNs;
+  unsigned stop = 0xFFFFFFFFu;  // rank, role and at, in 4, 2 and 26 bits
+};
+constexpr unsigned kStopAtBits = 26;
+__host__ __device__ __forceinline__ unsigned stop_key(int rank, int role) { return (unsigned)rank << 2 | (unsigned)role; }
+// The count at which this CTA's role stops.
+__device__ __forceinline__ unsigned stop_of(const MmWait& w, int rank, int role) {
+  return w.stop >> kStopAtBits == stop_key(rank, role) ? w.stop & ((1u << kStopAtBits) - 1) : 0xFFFFFFFFu;
+}
+
 // Bounded wait for a ring barrier, by the clock alone: the header's flags may
 // still hold what the workspace held before this launch.  CLUSTER: another CTA
 // signals the barrier too.
 template <bool CLUSTER>
-__device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned* flags) {
+__device__ __forceinline__ bool mm_wait(uint64_t* bar, unsigned parity, unsigned limit_ns, unsigned* flags) {
   auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
   if (done()) return true;
   const unsigned long long t0 = global_ns();
   while (!done()) {
-    if (global_ns() - t0 > kWaitLimitNs) {
+    if (global_ns() - t0 > limit_ns) {
       if (flags) atomicOr(flags, kFlagTimeout);
       return false;
     }
   }
   return true;
+}
+
+// mbar_drain where the phase is nearly always over: the clock is not read then.
+__device__ __forceinline__ void mm_drain(uint64_t* bar, unsigned parity) {
+  if (!mbar_try_wait(bar, parity)) mbar_drain(bar, parity);
 }
 
 // A place in the ring, kept by every role over all tiles of a CTA.
@@ -369,7 +390,8 @@ struct ScaleSlot {
 template <bool PAIR, int SLOTS, int U>
 __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0, int64_t rows,
                                            int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes, int block_bytes,
-                                           uint64_t* full, uint64_t* empty, unsigned* flags, uint32_t leader) {
+                                           uint64_t* full, uint64_t* empty, unsigned limit_ns, unsigned* flags,
+                                           unsigned stop, uint32_t leader) {
   const int lane = threadIdx.x & 31;
   const int last = (k0 + n - 1) / tiles_per_piece;
 #pragma unroll 1
@@ -377,8 +399,9 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
     if ((int)(t.piece & 1) != t.turn) continue;
     uint32_t w[4][8];
     load_scales<U>(s, row0, rows, nb, piece, w);
+    if (t.piece >= stop) return false;
     const unsigned use = t.piece / SLOTS, slot = t.piece - use * SLOTS;
-    if (!__all_sync(0xffffffffu, mm_wait<PAIR>(&empty[slot], (use & 1) ^ 1, flags))) return false;
+    if (!__all_sync(0xffffffffu, mm_wait<PAIR>(&empty[slot], (use & 1) ^ 1, limit_ns, flags))) return false;
     unsigned char* dst = ring + slot * slot_bytes + lane * 16;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -401,9 +424,11 @@ __device__ __forceinline__ bool scale_loop(ScaleTurn& t, int tiles_per_piece, co
 template <bool PAIR, int SLOTS, bool WIDE>
 __device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, int tiles_per_piece, const unsigned char* s, int64_t row0,
                                            int64_t rows, int64_t nb, int k0, int n, unsigned char* ring, int slot_bytes,
-                                           int block_bytes, uint64_t* full, uint64_t* empty, unsigned* flags, uint32_t leader) {
+                                           int block_bytes, uint64_t* full, uint64_t* empty, unsigned limit_ns, unsigned* flags,
+                                           unsigned stop, uint32_t leader) {
 #define DQ_SCALE_LOOP(U) \
-  scale_loop<PAIR, SLOTS, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, flags, leader)
+  scale_loop<PAIR, SLOTS, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, limit_ns, flags, stop, \
+                         leader)
   if (WIDE) return unit == 32 ? DQ_SCALE_LOOP(32) : DQ_SCALE_LOOP(16);
   return unit >= 8 ? DQ_SCALE_LOOP(8) : DQ_SCALE_LOOP(1);
 #undef DQ_SCALE_LOOP
@@ -415,11 +440,12 @@ struct MmLaunch {
   int unit_x, unit_w;  // powers of two that divide the scales' address and row
   int vec4;            // fours of outputs are aligned
   int early;           // the next grid may begin from the start on (else from the end of the multiply-adds on)
+  MmWait wait;
 };
 
 template <int FMT, int BN, bool WIDE>
 __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
-    k_matmul_tc(MatmulProblem p, MmLaunch l, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+    k_matmul_tc(const __grid_constant__ MatmulProblem p, const __grid_constant__ MmLaunch l, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   using G = MmGeo<FMT, BN>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
@@ -435,7 +461,8 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
   const int64_t nk = (p.K + F::kTileK - 1) / F::kTileK;
   const int64_t k0 = nk * rank / l.split;
   const int n = (int)(nk * (rank + 1) / l.split - k0);  // at least 1: split <= nk
-  unsigned* flags = p.flags;
+  unsigned* const flags = p.flags;
+  const unsigned limit_ns = l.wait.limit_ns;
   if (threadIdx.x == 0) {
     for (int i = 0; i < l.stages; ++i) {
       mbar_init(&full_t[i], 1);
@@ -466,21 +493,21 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
   float f1, f2;
   tensor_factors(p, f1, f2);
 
+  int issued = 0;            // of the lane that issues copies
+  uint64_t* last = nullptr;  // of the lane that issues multiply-adds: signalled when all are done
   if (warp == 0) {
     if (elect_one()) {
-      int slot = 0, issued = 0;
+      int slot = 0;
       unsigned phase = 1;
-      bool ok = true;
-      for (; issued < n; ++issued) {
-        if (!(ok = mm_wait<false>(&empty[slot], phase, flags))) break;
+      const unsigned stop = stop_of(l.wait, (int)rank, 0);
+      for (; issued < n && (unsigned)issued < stop; ++issued) {
+        if (!mm_wait<false>(&empty[slot], phase, limit_ns, flags)) break;
         unsigned char* st = ring + slot * G::kStage;
         mbar_arrive_expect_tx(&full_t[slot], G::kA + G::kB);
         tma_load_2d(st, &wmap, (int)((k0 + issued) * 128), (int)n0, &full_t[slot]);
         tma_load_2d(st + G::kA, &xmap, (int)((k0 + issued) * 128), (int)t0, &full_t[slot]);
         if (++slot == l.stages) slot = 0, phase ^= 1;
       }
-      if (!ok)  // the copies in flight land before the CTA leaves
-        for (int i = max(0, issued - l.stages); i < issued; ++i) mbar_drain(&full_t[i % l.stages], (i / l.stages) & 1);
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -489,8 +516,8 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
       int it = 0;
       for (; it < n; ++it) {
         const int kt = (int)k0 + it, u = kt % F::kPiece;
-        if ((it == 0 || u == 0) && !mm_wait<false>(&full_s[piece.slot], piece.phase, flags)) break;
-        if (!mm_wait<false>(&full_t[at.slot], at.phase, flags)) break;
+        if ((it == 0 || u == 0) && !mm_wait<false>(&full_s[piece.slot], piece.phase, limit_ns, flags)) break;
+        if (!mm_wait<false>(&full_t[at.slot], at.phase, limit_ns, flags)) break;
         tc_fence_after();
         const uint32_t st = smem_u32(ring + at.slot * G::kStage);
         const uint32_t sfa = smem_u32(scales + piece.slot * G::kScales) + 512 * u * F::kAtoms, sfb = sfa + 4096;
@@ -511,18 +538,15 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
         }
         at.next(l.stages);
       }
-      if (it == n) {
-        tc_commit<1>(&acc_full);
-      } else {  // the tile is not finished, so its readers' wait runs out too; what was issued ends before the CTA does
-        tc_commit<1>(&given_up);
-        mbar_drain(&given_up, 0);
-      }
+      last = it == n ? &acc_full : &given_up;  // an unfinished tile's readers' wait runs out too
+      tc_commit<1>(last);
     }
   } else {
     const bool of_w = (warp & 1) == 0;
     ScaleTurn t{(warp - 2) >> 1};
     scale_warp<false, kScaleSlots, WIDE>(of_w ? l.unit_w : l.unit_x, t, F::kPiece, of_w ? p.ws : p.xs, of_w ? n0 : t0, of_w ? p.N : p.T,
-                      p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, flags, 0u);
+                      p.K / F::kGroup, (int)k0, n, scales + (of_w ? 0 : 4096), G::kScales, 512, full_s, empty_s, limit_ns, flags,
+                      stop_of(l.wait, (int)rank, of_w ? 1 : 2), 0u);
   }
   __syncwarp();
 
@@ -538,7 +562,7 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
   bool ok = true;
   if (l.split > 1) cluster_wait();  // every CTA of the cluster has begun
   if (warp >= 2) {
-    ok = __all_sync(0xffffffffu, mm_wait<false>(&acc_full, 0, flags));
+    ok = __all_sync(0xffffffffu, mm_wait<false>(&acc_full, 0, limit_ns, flags));
     tc_fence_after();
     const int q = warp & 3;
     const int64_t nn = n0 + 32 * q + lane;
@@ -582,6 +606,14 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
     }
     tc_fence_before();
   }
+  // Whatever the waits did, all copies and multiply-adds that were issued are done before the CTA gives back its memory.
+  // (A lane a slot: one after the other they took 0.2 us.)
+  if (warp == 0) {
+    issued = __reduce_max_sync(0xffffffffu, issued);
+    if (lane < min(issued, l.stages)) mm_drain(&full_t[lane], ((issued - 1 - lane) / l.stages) & 1);
+  }
+  if (last) mm_drain(last, 0);
+  __syncwarp();
   if (l.split > 1) {
     cluster_sync();
     const int first = (int)rank * share, total = min(share, tv - first) * 32;  // groups of four features
@@ -651,6 +683,7 @@ struct PairLaunch {
   int rows16;  // rows of Y start at multiples of 16 bytes
   int vec4;   // fours of outputs are aligned
   int split;  // pairs of a cluster, each with its share of the K tiles of one tile
+  MmWait wait;
 };
 constexpr int kPartPitch = 260;  // floats of a partial tile's row in shared memory: conflict-free both ways
 
@@ -733,6 +766,22 @@ static __device__ __noinline__ void pair_give_up(const MatmulProblem& p, const P
   }
 }
 
+// Waits until the last copies of both CTAs of a pair that gave up have landed: tile i of `even` or `odd` copied so far
+// went to slot i % kPairStages, both halves of `half` bytes reported to the even CTA's barrier `full`, which may lack
+// the even CTA's arrival or one half.  (Neither is more than kPairStages tiles ahead: those need the other's to be
+// consumed first.)
+static __device__ __noinline__ void pair_drain(uint64_t* full, unsigned even, unsigned odd, unsigned half) {
+  const unsigned last = max(even, odd);
+  for (unsigned i = last > kPairStages ? last - kPairStages : 0; i < last; ++i) {
+    uint64_t* bar = &full[i % kPairStages];
+    if (i >= even)
+      mbar_arrive_expect_tx(bar, half);
+    else if (i >= odd)
+      mbar_complete_tx(bar, half);
+    mbar_drain(bar, i / kPairStages & 1);
+  }
+}
+
 template <int FMT, bool OUT32, bool WIDE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     k_matmul_pair(const __grid_constant__ MatmulProblem p, const __grid_constant__ PairLaunch l, const __grid_constant__ CUtensorMap wmap,
@@ -741,8 +790,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
   __shared__ uint64_t full_t[kPairStages], empty[kPairStages], full_s[G::kSlots], empty_s[G::kSlots], acc_full, acc_empty,
-      given_up;
+      done;
   __shared__ uint32_t tmem_base;
+  __shared__ unsigned failed, copied[2];  // a wait of the cluster ran out; K tiles that the pair's CTAs copied (in the even one)
   unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)mm_smem + 1023) & ~(uintptr_t)1023);
   unsigned char* scales = ring + kPairStages * G::kStage;
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
@@ -752,7 +802,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int all_k = (int)((p.K + F::kTileK - 1) / F::kTileK);
   const int k0 = (int)((int64_t)all_k * share / l.split), k1 = (int)((int64_t)all_k * (share + 1) / l.split);
   const int64_t nb = p.K / F::kGroup;
-  unsigned* flags = p.flags;
+  unsigned* const flags = p.flags;
+  const unsigned limit_ns = l.wait.limit_ns;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kPairStages; ++i) {
       mbar_init(&full_t[i], 1);
@@ -763,9 +814,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       mbar_init(&empty_s[i], 1);
     }
     mbar_init(&acc_full, 1);
-    mbar_init(&given_up, 1);
+    mbar_init(&done, 1);
     mbar_init(&acc_empty, 2 * kPairEpilogue);
     mbar_fence_init();
+    failed = 0;
   }
   if (warp == 9) tc_alloc<2, 512>(smem_u32(&tmem_base));
   tc_fence_before();
@@ -781,17 +833,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   griddep_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && flags && l.first == 0) *reinterpret_cast<volatile unsigned*>(flags) = 0;
   MmSlot at;
-  bool gave_up = false;
+  // tells every CTA of the cluster (in a self-test too, where nothing runs out in the role that stops)
+  auto give_up = [&] {
+    for (int r = 0; r < 2 * l.split; ++r) st_cluster_if(true, smem_u32(&failed), (uint32_t)r, 1u);
+  };
 
   if (warp == 8) {
     if (elect_one()) {
       bool ok = true;
-      int64_t issued = 0;
+      unsigned issued = 0;
+      const unsigned stop = stop_of(l.wait, in_cluster, 0);
       for (unsigned i = l.first + pair; i < l.end && ok; i += pairs) {
         int64_t m, n;
         pair_tile(l, i, m, n);
         for (int kt = k0; kt < k1; ++kt, ++issued) {
-          if (!(ok = mm_wait<true>(&empty[at.slot], at.phase ^ 1, flags))) break;
+          if (!(ok = issued < stop && mm_wait<true>(&empty[at.slot], at.phase ^ 1, limit_ns, flags))) break;
           unsigned char* st = ring + at.slot * G::kStage;
           if (rank == 0) mbar_arrive_expect_tx(&full_t[at.slot], 2 * (G::kA + G::kB));
           tma_load_2d_pair(st, &xmap, kt * 128, (int)(m * 256 + rank * 128), &full_t[at.slot]);
@@ -799,9 +855,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           at.next(kPairStages);
         }
       }
-      if (!ok && rank == 0)  // both CTAs' copies land before the pair leaves
-        for (int64_t i = max((int64_t)0, issued - kPairStages); i < issued; ++i)
-          mbar_drain(&full_t[i % kPairStages], (unsigned)(i / kPairStages) & 1);
+      st_cluster_if(true, smem_u32(&copied[rank]), leader, issued);
+      if (!ok) give_up();
+      for (unsigned i = issued > kPairStages ? issued - kPairStages : 0; ok && i < issued; ++i)  // the last slots' releases
+        ok = mm_wait<true>(&empty[i % kPairStages], i / kPairStages & 1, limit_ns, flags);
     }
   } else if (warp == 9) {
     if (rank == 0 && elect_one()) {
@@ -809,12 +866,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       ScaleSlot<G::kSlots> piece;
       bool ok = true;
       for (unsigned i = l.first + pair; i < l.end && ok; i += pairs, turn ^= 1) {
-        if (!(ok = mm_wait<true>(&acc_empty, turn ^ 1, flags))) break;
+        if (!(ok = mm_wait<true>(&acc_empty, turn ^ 1, limit_ns, flags))) break;
         tc_fence_after();
         for (int kt = k0; kt < k1; ++kt, set ^= 1) {
           const int u = kt % F::kPiece;
-          if ((u == 0 || kt == k0) && !(ok = mm_wait<true>(&full_s[piece.slot], piece.phase, flags))) break;
-          if (!(ok = mm_wait<true>(&full_t[at.slot], at.phase, flags))) break;
+          if ((u == 0 || kt == k0) && !(ok = mm_wait<true>(&full_s[piece.slot], piece.phase, limit_ns, flags))) break;
+          if (!(ok = mm_wait<true>(&full_t[at.slot], at.phase, limit_ns, flags))) break;
           tc_fence_after();
           const uint32_t st = smem_u32(ring + at.slot * G::kStage);
           const uint32_t sa = smem_u32(scales + piece.slot * G::kScales) + 512 * u * F::kAtoms;
@@ -840,10 +897,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (ok) tc_commit<2>(&acc_full, leader);
       }
-      if (!ok) {  // as above
-        tc_commit<2>(&given_up, leader);
-        mbar_drain(&given_up, 0);
-      }
+      if (!ok) give_up();
+      tc_commit<2>(&done, leader);
     }
   } else if (warp >= 10) {
     const int block = (warp - 10) >> 1;  // 0: the tokens, 1 and 2: the features' halves
@@ -856,8 +911,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       ok = scale_warp<true, G::kSlots, WIDE>(of_x ? l.unit_x : l.unit_w, t, F::kPiece, of_x ? p.xs : p.ws,
                             of_x ? m * 256 + rank * 128 : n * 256 + (block - 1) * 128, of_x ? p.T : p.N, nb, k0, k1 - k0,
                             scales + (of_x ? 0 : 4096 + (block - 1) * 512), G::kScales, of_x ? 512 : 1024, full_s, empty_s,
-                            flags, leader);
+                            limit_ns, flags, stop_of(l.wait, in_cluster, of_x ? 2 : 1), leader);
     }
+    if (!ok && lane == 0) give_up();
   } else {
     float f1, f2_;
     tensor_factors(p, f1, f2_);
@@ -867,11 +923,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (unsigned i = l.first + pair; i < l.end; i += pairs, turn ^= 1) {
       int64_t m, n;
       pair_tile(l, i, m, n);
-      if (!__all_sync(0xffffffffu, mm_wait<true>(&acc_full, turn, flags))) {
-        if (l.split > 1)
-          gave_up = true;
-        else
-          pair_give_up<OUT32>(p, l, i, pairs, rank, warp);
+      if (!__all_sync(0xffffffffu, mm_wait<true>(&acc_full, turn, limit_ns, flags))) {
+        if (lane == 0) give_up();
+        if (l.split == 1) pair_give_up<OUT32>(p, l, i, pairs, rank, warp);
         break;
       }
       tc_fence_after();
@@ -936,11 +990,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   __syncwarp();
   if (l.split > 1) {
     // each CTA joins and stores its share of the 128 rows, as many as there are, that the pairs' CTAs of its rank hold, in pair order
-    if (__any_sync(0xffffffffu, gave_up))
-      for (int e = lane; e < 32 * 128; e += 32)  // a wait ran out: no number that looks like a result
-        reinterpret_cast<float*>(ring)[(32 * (warp & 3) + (e >> 7)) * kPartPitch + 128 * (warp >> 2) + (e & 127)] =
-            __uint_as_float(0x7FC00000u);
     cluster_sync();
+    const bool nothing = ld_volatile(&failed) != 0;  // a wait ran out: no number that looks like a result
     float f1, f2_;
     tensor_factors(p, f1, f2_);
     int64_t m, n;
@@ -959,12 +1010,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
       for (int r = 1; r < 4; ++r)
         if (r < l.split) sum.x += v[r].x, sum.y += v[r].y, sum.z += v[r].z, sum.w += v[r].w;
+      if (nothing) sum = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
       const float o[4] = {sum.x * f1 * f2_, sum.y * f1 * f2_, sum.z * f1 * f2_, sum.w * f1 * f2_};
       y_store4(p.y, p.y_dt, t * p.N + nn, o, p.N - nn, l.vec4);
     }
   }
+  // all multiply-adds that were issued are done, whether their readers waited for them or not
+  if (warp == 0 && elect_one()) mm_drain(&done, 0);
+  __syncwarp();
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still signal it or read its shared memory
+  if (ld_volatile(&failed) != 0) {  // the same in all CTAs
+    if (rank == 0 && warp == 8 && elect_one()) pair_drain(full_t, copied[0], copied[1], G::kA + G::kB);
+    __syncwarp();
+    cluster_sync();
+  }
   if (warp == 9) {
     tc_fence_after();
     tc_dealloc<2, 512>(tmem);
@@ -1003,7 +1063,7 @@ static bool vec4_rows(const MatmulProblem& p) {
 }
 
 template <int FMT, int BN>
-static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
+static cudaError_t matmul_tc(const MatmulProblem& p, const MmWait& wait, int sms, cudaStream_t st) {
   using G = MmGeo<FMT, BN>;
   CUtensorMap wmap, xmap;
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
@@ -1012,6 +1072,7 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
   const int64_t tiles = (p.N + 127) / 128 * ((p.T + BN - 1) / BN);
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
   MmLaunch l;
+  l.wait = wait;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
   l.vec4 = vec4_rows(p);
@@ -1057,13 +1118,14 @@ static cudaError_t matmul_tc(const MatmulProblem& p, int sms, cudaStream_t st) {
 // (1500 x 4096 x 14336 MXFP8, 96 tiles on 74 pairs: 82 us as two waves, 72 so;
 // 2048 x 14336 x 4096 NVFP4, 448 tiles: 62 us as seven waves, 66 so.)
 template <int FMT, bool OUT32>
-static cudaError_t matmul_pair(const MatmulProblem& p, int sms, cudaStream_t st) {
+static cudaError_t matmul_pair(const MatmulProblem& p, const MmWait& wait, int sms, cudaStream_t st) {
   using G = PairGeo<FMT>;
   CUtensorMap wmap, xmap;
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
   if (!encode_codes(&wmap, p.wq, row_bytes, p.N, 128) || !encode_codes(&xmap, p.xq, row_bytes, p.T, 128))
     return cudaErrorInvalidValue;
   PairLaunch l;
+  l.wait = wait;
   l.tiles_m = (unsigned)((p.T + 255) / 256);
   l.tiles_n = (unsigned)((p.N + 255) / 256);
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
@@ -1123,23 +1185,21 @@ static int64_t pair_ns(const MatmulProblem& p, int fmt, int64_t nk, int sms) {
 }
 
 template <int FMT>
-static cudaError_t matmul_fmt(const MatmulProblem& p, int sms, cudaStream_t st) {
+static cudaError_t matmul_fmt(const MatmulProblem& p, const MmWait& wait, int sms, cudaStream_t st) {
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
   if (((uintptr_t)p.xq | (uintptr_t)p.wq | (uintptr_t)row_bytes) % 16 != 0) return matmul_any<FMT>(p, st);
-  if (p.T <= 16) return matmul_tc<FMT, 16>(p, sms, st);
-  if (p.T <= 32) return matmul_tc<FMT, 32>(p, sms, st);
+  if (p.T <= 16) return matmul_tc<FMT, 16>(p, wait, sms, st);
+  if (p.T <= 32) return matmul_tc<FMT, 32>(p, wait, sms, st);
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
   const int64_t t64 = tc_ns(p, FMT, nk, 64, sms), t128 = tc_ns(p, FMT, nk, 128, sms), two = pair_ns(p, FMT, nk, sms);
-  if (p.T <= 64 || (t64 <= t128 && t64 <= two)) return matmul_tc<FMT, 64>(p, sms, st);
+  if (p.T <= 64 || (t64 <= t128 && t64 <= two)) return matmul_tc<FMT, 64>(p, wait, sms, st);
   // 128 tokens a tile leave no shared memory for a second CTA of an SM
-  if ((p.N + 127) / 128 * ((p.T + 127) / 128) <= sms && t128 <= two) return matmul_tc<FMT, 128>(p, sms, st);
-  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, sms, st) : matmul_pair<FMT, false>(p, sms, st);
+  if ((p.N + 127) / 128 * ((p.T + 127) / 128) <= sms && t128 <= two) return matmul_tc<FMT, 128>(p, wait, sms, st);
+  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, wait, sms, st) : matmul_pair<FMT, false>(p, wait, sms, st);
 }
 
-}  // namespace dq
-
-extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format,
-                         int group, void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+static int matmul_call(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format, int group,
+                       void* Y, int y_dtype, void* workspace, size_t workspace_bytes, const MmWait& wait, void* stream) {
   if (tokens <= 0 || rows <= 0 || cols <= 0 || group <= 0 || cols % group != 0) return DQ_EINVAL;
   if (format < DQ_INT4 || format > DQ_MXFP8) return DQ_EINVAL;
   if (format != DQ_NVFP4 && format != DQ_MXFP4 && format != DQ_MXFP8) return DQ_EUNSUPPORTED;
@@ -1155,7 +1215,7 @@ extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* 
   if ((uintptr_t)Y % (y_dtype == DQ_F32 ? 4 : 2) != 0) return DQ_EINVAL;
   if ((uintptr_t)workspace % 256 != 0) return DQ_EINVAL;
   if (workspace && workspace_bytes < DQ_MATMUL_WORKSPACE_BYTES) return DQ_EWORKSPACE;
-  dq::MatmulProblem p{};
+  MatmulProblem p{};
   p.xq = static_cast<const unsigned char*>(X->codes);
   p.xs = static_cast<const unsigned char*>(X->block_scales);
   p.wq = static_cast<const unsigned char*>(W->codes);
@@ -1169,13 +1229,34 @@ extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* 
   p.T = tokens;
   p.N = rows;
   p.K = cols;
-  p.flags = workspace ? &static_cast<dq::WsHeader*>(workspace)->flags : nullptr;
+  p.flags = workspace ? &static_cast<WsHeader*>(workspace)->flags : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ECUDA;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DQ_ECUDA;
-  const cudaError_t e = format == DQ_NVFP4   ? dq::matmul_fmt<dq::FMT_NVFP4>(p, sms, s)
-                        : format == DQ_MXFP4 ? dq::matmul_fmt<dq::FMT_MXFP4>(p, sms, s)
-                                             : dq::matmul_fmt<dq::FMT_MXFP8>(p, sms, s);
+  const cudaError_t e = format == DQ_NVFP4   ? matmul_fmt<FMT_NVFP4>(p, wait, sms, s)
+                        : format == DQ_MXFP4 ? matmul_fmt<FMT_MXFP4>(p, wait, sms, s)
+                                             : matmul_fmt<FMT_MXFP8>(p, wait, sms, s);
   return e == cudaSuccess ? DQ_OK : DQ_ECUDA;
+}
+
+}  // namespace dq
+
+extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format,
+                         int group, void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  return dq::matmul_call(X, tokens, W, rows, cols, format, group, Y, y_dtype, workspace, workspace_bytes, dq::MmWait(),
+                         stream);
+}
+
+extern "C" int dq_matmul_selftest(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols,
+                                  int format, int group, void* Y, int y_dtype, void* workspace, size_t workspace_bytes,
+                                  unsigned wait_ns, int rank, int role, unsigned at, void* stream) {
+  if (wait_ns < 1000000u || wait_ns > dq::kWaitLimitNs || rank < 0 || rank > 7 || role < 0 || role > 2 ||
+      at >> dq::kStopAtBits != 0 || !workspace)
+    return DQ_EINVAL;
+  dq::MmWait wait;
+  wait.limit_ns = wait_ns;
+  wait.stop = dq::stop_key(rank, role) << dq::kStopAtBits | at;
+  return dq::matmul_call(X, tokens, W, rows, cols, format, group, Y, y_dtype, workspace, workspace_bytes,
+                         wait, stream);
 }

@@ -162,6 +162,11 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, unsigned pa
   return ok != 0;
 }
 
+// `bytes` of a barrier's expected copies that will not come.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, unsigned bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // 16 consecutive columns of this warp's lane quarter, one lane a thread.
 __device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t* v) {
   asm volatile(

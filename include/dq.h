@@ -330,6 +330,19 @@ int dq_act_quant(const void* X, int x_dtype, int64_t rows, int64_t cols, const v
 int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format, int group,
               void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Self-test of dq_matmul's bounded device waits (no counterpart in the method;
+ * failure detection): dq_matmul with waits of wait_ns (10^6 .. 10^9, instead of
+ * a second) in which one role of the CTA `rank` (0 .. 7) of every cluster stops as if its
+ * wait had run out: role 0 the copies of codes, after `at` (below 2^26) K tiles; 1 the
+ * weights' and 2 the tokens' block scales, after `at` pieces of 32 bytes a row.
+ * The waits that depend on it run out, every output whose sum is not finished
+ * is NaN, the others are dq_matmul's, and dq_sync_status returns DQ_ECUDA; where
+ * there is no such CTA or piece it is a plain dq_matmul.  The workspace is
+ * needed; the kernel for codes of any alignment has no waits. */
+int dq_matmul_selftest(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format,
+                       int group, void* Y, int y_dtype, void* workspace, size_t workspace_bytes, unsigned wait_ns, int rank,
+                       int role, unsigned at, void* stream);
+
 /* Device workspace bytes of dq_norm_quant (0 on invalid arguments): a header
  * and, for DQ_NVFP4, 8 bytes per row.  Alignment: 256 bytes. */
 size_t dq_norm_workspace_bytes(int64_t rows, int64_t cols, int format, int group);
