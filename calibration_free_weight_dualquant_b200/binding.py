@@ -68,6 +68,11 @@ class _Matrix(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("out", _Outputs)]
 
 
+class _MatmulInfo(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int), ("tile_tokens", ctypes.c_int), ("aligned_scales", ctypes.c_int),
+                ("whole_tiles", ctypes.c_int64), ("split_tiles", ctypes.c_int64), ("split", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -115,6 +120,8 @@ def load_library():
     lib.dq_matmul.restype = I
     lib.dq_matmul_selftest.argtypes = lib.dq_matmul.argtypes[:-1] + [ctypes.c_uint, I, I, ctypes.c_uint, P]
     lib.dq_matmul_selftest.restype = I
+    lib.dq_matmul_kernel.argtypes = lib.dq_matmul.argtypes[:-3] + [ctypes.POINTER(_MatmulInfo)]
+    lib.dq_matmul_kernel.restype = I
     lib.dq_norm_workspace_bytes.argtypes = [I64, I64, I, I]
     lib.dq_norm_workspace_bytes.restype = SZ
     lib.dq_norm_quant.argtypes = [P, P, I, I64, I64, P, ctypes.c_float, P, I, I, I, ctypes.POINTER(_Outputs), P, P, SZ,
@@ -434,18 +441,34 @@ def dq_matmul(X: dict, W: dict, fmt, group: Optional[int] = None, out: Optional[
     return _call(codes.device, stream, m.matmul, X, W, f, out, dt, workspace, bool(check))
 
 
+def _product_args(X: dict, W: dict, fmt, out: torch.Tensor) -> tuple:
+    """The arguments of dq_matmul up to the output's type, for the calls that test and describe it."""
+    f = _fmt(fmt)
+    x, w = (_Outputs(q["codes"].data_ptr(), q["block_scales"].data_ptr(),
+                     q["tensor_scale"].data_ptr() if f == Format.NVFP4 else None, None, None) for q in (X, W))
+    cols = X["codes"].shape[1] * (1 if f == Format.MXFP8 else 2)
+    return (ctypes.byref(x), X["codes"].shape[0], ctypes.byref(w), W["codes"].shape[0], cols, int(f), DEFAULT_GROUP[f],
+            out.data_ptr(), _DTYPES[out.dtype])
+
+
+def matmul_kernel(X: dict, W: dict, fmt, out: torch.Tensor) -> dict:
+    """Which kernel dq_matmul into ``out`` runs on the current device and how it divides the work (dq_matmul_kernel):
+    {"kernel": "any", "tile" or "pair", "tile_tokens", "aligned_scales", "whole_tiles", "split_tiles", "split"}."""
+    info = _MatmulInfo()
+    st = load_library().dq_matmul_kernel(*_product_args(X, W, fmt, out), ctypes.byref(info))
+    if st != 0:
+        raise DQError(st, "dq_matmul_kernel")
+    d = {name: getattr(info, name) for name, _ in info._fields_}
+    return {**d, "kernel": ("any", "tile", "pair")[info.kernel], "aligned_scales": bool(info.aligned_scales)}
+
+
 def matmul_selftest(X: dict, W: dict, fmt, out: torch.Tensor, workspace: torch.Tensor, rank: int, role: int, at: int,
                     wait_ns: int = 2_000_000, stream=None) -> int:
     """dq_matmul into ``out`` with one role of a CTA withheld (dq_matmul_selftest) on the current device; returns the
     status it leaves in ``workspace``: DQ_ECUDA (5) where a wait ran out."""
     lib = load_library()
-    f = _fmt(fmt)
-    x, w = (_Outputs(q["codes"].data_ptr(), q["block_scales"].data_ptr(),
-                     q["tensor_scale"].data_ptr() if f == Format.NVFP4 else None, None, None) for q in (X, W))
-    cols = X["codes"].shape[1] * (1 if f == Format.MXFP8 else 2)
-    st = lib.dq_matmul_selftest(ctypes.byref(x), X["codes"].shape[0], ctypes.byref(w), W["codes"].shape[0], cols, int(f),
-                                DEFAULT_GROUP[f], out.data_ptr(), _DTYPES[out.dtype], workspace.data_ptr(),
-                                workspace.numel(), wait_ns, rank, role, at, _stream_ptr(stream))
+    st = lib.dq_matmul_selftest(*_product_args(X, W, fmt, out), workspace.data_ptr(), workspace.numel(), wait_ns, rank,
+                                role, at, _stream_ptr(stream))
     if st != 0:
         raise DQError(st, "dq_matmul_selftest")
     return lib.dq_sync_status(workspace.data_ptr(), _stream_ptr(stream))

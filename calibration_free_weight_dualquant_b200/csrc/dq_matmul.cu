@@ -173,12 +173,6 @@ __global__ void __launch_bounds__(256) k_matmul_any(MatmulProblem p) {
     }
 }
 
-template <int FMT>
-static cudaError_t matmul_any(const MatmulProblem& p, cudaStream_t st) {
-  const int64_t tiles = (p.T + 63) / 64 * ((p.N + 63) / 64);
-  return launch_early(k_matmul_any<FMT>, (unsigned)tiles, 256, 0, 1, st, p);
-}
-
 // ---------------------------------------------------------------------------
 // Tensor-core product: a CTA computes the tile of 128 output features and BN
 // tokens, Y^T = W X^T, so that few tokens still fill the tensor core's 128
@@ -1031,6 +1025,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   }
 }
 
+// What a call brings along on the host.
+struct MmCall {
+  int sms;
+  cudaStream_t st;
+  MmWait wait;
+  dq_matmul_info* info;  // if given, what would run goes here and nothing does
+};
+
 // 2-D tensor map of a code matrix in bytes: boxes of 128 bytes x `box_rows`
 // rows in the 128-byte swizzle, zeros outside.
 static bool encode_codes(CUtensorMap* map, const unsigned char* q, int64_t row_bytes, int64_t rows, int box_rows) {
@@ -1062,8 +1064,18 @@ static bool vec4_rows(const MatmulProblem& p) {
   return p.N % 4 == 0 && (uintptr_t)p.y % (p.y_dt == DT_F32 ? 16 : 8) == 0;
 }
 
+template <int FMT>
+static cudaError_t matmul_any(const MatmulProblem& p, const MmCall& c) {
+  const int64_t tiles = (p.T + 63) / 64 * ((p.N + 63) / 64);
+  if (c.info) {
+    *c.info = {DQ_MATMUL_ANY, 64, 0, tiles, 0, 1};
+    return cudaSuccess;
+  }
+  return launch_early(k_matmul_any<FMT>, (unsigned)tiles, 256, 0, 1, c.st, p);
+}
+
 template <int FMT, int BN>
-static cudaError_t matmul_tc(const MatmulProblem& p, const MmWait& wait, int sms, cudaStream_t st) {
+static cudaError_t matmul_tc(const MatmulProblem& p, const MmCall& c) {
   using G = MmGeo<FMT, BN>;
   CUtensorMap wmap, xmap;
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
@@ -1072,7 +1084,7 @@ static cudaError_t matmul_tc(const MatmulProblem& p, const MmWait& wait, int sms
   const int64_t tiles = (p.N + 127) / 128 * ((p.T + BN - 1) / BN);
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
   MmLaunch l;
-  l.wait = wait;
+  l.wait = c.wait;
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
   l.unit_w = scale_unit(p.ws, p.K / TcFormat<FMT>::kGroup);
   l.vec4 = vec4_rows(p);
@@ -1087,11 +1099,11 @@ static cudaError_t matmul_tc(const MatmulProblem& p, const MmWait& wait, int sms
   // The largest split whose clusters all run at once (some SMs of a GPC are left
   // over by clusters that do not divide it: 132 of 148 SMs hold clusters of 4 or 6,
   // 120 of 8, 105 of 7; 40 x 2048 x 5632 MXFP4, 16 tiles: 15.2 us split in 7, 8.4 in 6).
-  for (l.split = (int)min((int64_t)8, min(nk, max((int64_t)1, sms / tiles)));; --l.split) {
+  for (l.split = (int)min((int64_t)8, min(nk, max((int64_t)1, c.sms / tiles)));; --l.split) {
     const int64_t per = (nk + l.split - 1) / l.split;
     const int fixed = kScaleSlots * G::kScales + 1024 + (l.split > 1 ? (BN + l.split - 1) / l.split * l.split * 512 : 0);
     // one CTA an SM takes all shared memory, more tiles share an SM by three
-    const int room = ((tiles * l.split <= sms ? kMmSmem : 74 * 1024) - fixed) / G::kStage;
+    const int room = ((tiles * l.split <= c.sms ? kMmSmem : 74 * 1024) - fixed) / G::kStage;
     l.stages = (int)min((int64_t)kMmMaxStages, min(per, (int64_t)room));
     smem = l.stages * G::kStage + fixed;
     // A CTA takes at least its tensor memory's share of the SM's shared memory
@@ -1107,9 +1119,13 @@ static cudaError_t matmul_tc(const MatmulProblem& p, const MmWait& wait, int sms
     if ((e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg)) != cudaSuccess) return e;
     if (clusters >= tiles) break;
   }
+  if (c.info) {
+    *c.info = {DQ_MATMUL_TILE, BN, l.unit_x >= 16 && l.unit_w >= 16, l.split > 1 ? 0 : tiles, l.split > 1 ? tiles : 0, l.split};
+    return cudaSuccess;
+  }
   // where an SM takes several CTAs, those of the next grid would take the places of this one unevenly
-  l.early = tiles * l.split <= sms;
-  return launch_early(kern, (unsigned)(tiles * l.split), kMmThreads, (size_t)smem, l.split, st, p, l, wmap, xmap);
+  l.early = tiles * l.split <= c.sms;
+  return launch_early(kern, (unsigned)(tiles * l.split), kMmThreads, (size_t)smem, l.split, c.st, p, l, wmap, xmap);
 }
 
 // Whole waves of pairs first; the tiles left over, or all of them where they do
@@ -1118,14 +1134,14 @@ static cudaError_t matmul_tc(const MatmulProblem& p, const MmWait& wait, int sms
 // (1500 x 4096 x 14336 MXFP8, 96 tiles on 74 pairs: 82 us as two waves, 72 so;
 // 2048 x 14336 x 4096 NVFP4, 448 tiles: 62 us as seven waves, 66 so.)
 template <int FMT, bool OUT32>
-static cudaError_t matmul_pair(const MatmulProblem& p, const MmWait& wait, int sms, cudaStream_t st) {
+static cudaError_t matmul_pair(const MatmulProblem& p, const MmCall& c) {
   using G = PairGeo<FMT>;
   CUtensorMap wmap, xmap;
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
   if (!encode_codes(&wmap, p.wq, row_bytes, p.N, 128) || !encode_codes(&xmap, p.xq, row_bytes, p.T, 128))
     return cudaErrorInvalidValue;
   PairLaunch l;
-  l.wait = wait;
+  l.wait = c.wait;
   l.tiles_m = (unsigned)((p.T + 255) / 256);
   l.tiles_n = (unsigned)((p.N + 255) / 256);
   l.unit_x = scale_unit(p.xs, p.K / TcFormat<FMT>::kGroup);
@@ -1135,7 +1151,7 @@ static cudaError_t matmul_pair(const MatmulProblem& p, const MmWait& wait, int s
   auto kern = l.unit_x >= 16 && l.unit_w >= 16 ? k_matmul_pair<FMT, OUT32, true> : k_matmul_pair<FMT, OUT32, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
   if (e != cudaSuccess) return e;
-  const unsigned tiles = l.tiles_m * l.tiles_n, pairs = (unsigned)sms / 2;
+  const unsigned tiles = l.tiles_m * l.tiles_n, pairs = (unsigned)c.sms / 2;
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
   const unsigned rest = tiles % pairs;
   int split = 1;
@@ -1150,17 +1166,21 @@ static cudaError_t matmul_pair(const MatmulProblem& p, const MmWait& wait, int s
     if ((unsigned)room >= rest) split = s;
   }
   const unsigned whole = split > 1 ? tiles - rest : tiles;
+  if (c.info) {
+    *c.info = {DQ_MATMUL_PAIR, 256, l.unit_x >= 16 && l.unit_w >= 16, whole, tiles - whole, split};
+    return cudaSuccess;
+  }
   if (whole > 0) {
     l.first = 0;
     l.end = whole;
     l.split = 1;
-    e = launch_early(kern, 2 * (whole < pairs ? whole : pairs), kPairThreads, (size_t)G::kSmem, 2, st, p, l, wmap, xmap);
+    e = launch_early(kern, 2 * (whole < pairs ? whole : pairs), kPairThreads, (size_t)G::kSmem, 2, c.st, p, l, wmap, xmap);
     if (e != cudaSuccess || whole == tiles) return e;
   }
   l.first = whole;
   l.end = tiles;
   l.split = split;
-  return launch_early(kern, rest * 2 * split, kPairThreads, (size_t)G::kSmem, 2 * split, st, p, l, wmap, xmap);
+  return launch_early(kern, rest * 2 * split, kPairThreads, (size_t)G::kSmem, 2 * split, c.st, p, l, wmap, xmap);
 }
 
 // About how long a product takes, in ns, to choose between the kernels: a fixed
@@ -1185,21 +1205,22 @@ static int64_t pair_ns(const MatmulProblem& p, int fmt, int64_t nk, int sms) {
 }
 
 template <int FMT>
-static cudaError_t matmul_fmt(const MatmulProblem& p, const MmWait& wait, int sms, cudaStream_t st) {
+static cudaError_t matmul_fmt(const MatmulProblem& p, const MmCall& c) {
   const int64_t row_bytes = FMT == FMT_MXFP8 ? p.K : p.K / 2;
-  if (((uintptr_t)p.xq | (uintptr_t)p.wq | (uintptr_t)row_bytes) % 16 != 0) return matmul_any<FMT>(p, st);
-  if (p.T <= 16) return matmul_tc<FMT, 16>(p, wait, sms, st);
-  if (p.T <= 32) return matmul_tc<FMT, 32>(p, wait, sms, st);
+  if (((uintptr_t)p.xq | (uintptr_t)p.wq | (uintptr_t)row_bytes) % 16 != 0) return matmul_any<FMT>(p, c);
+  if (p.T <= 16) return matmul_tc<FMT, 16>(p, c);
+  if (p.T <= 32) return matmul_tc<FMT, 32>(p, c);
   const int64_t nk = (p.K + TcFormat<FMT>::kTileK - 1) / TcFormat<FMT>::kTileK;
-  const int64_t t64 = tc_ns(p, FMT, nk, 64, sms), t128 = tc_ns(p, FMT, nk, 128, sms), two = pair_ns(p, FMT, nk, sms);
-  if (p.T <= 64 || (t64 <= t128 && t64 <= two)) return matmul_tc<FMT, 64>(p, wait, sms, st);
+  const int64_t t64 = tc_ns(p, FMT, nk, 64, c.sms), t128 = tc_ns(p, FMT, nk, 128, c.sms), two = pair_ns(p, FMT, nk, c.sms);
+  if (p.T <= 64 || (t64 <= t128 && t64 <= two)) return matmul_tc<FMT, 64>(p, c);
   // 128 tokens a tile leave no shared memory for a second CTA of an SM
-  if ((p.N + 127) / 128 * ((p.T + 127) / 128) <= sms && t128 <= two) return matmul_tc<FMT, 128>(p, wait, sms, st);
-  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, wait, sms, st) : matmul_pair<FMT, false>(p, wait, sms, st);
+  if ((p.N + 127) / 128 * ((p.T + 127) / 128) <= c.sms && t128 <= two) return matmul_tc<FMT, 128>(p, c);
+  return p.y_dt == DT_F32 ? matmul_pair<FMT, true>(p, c) : matmul_pair<FMT, false>(p, c);
 }
 
 static int matmul_call(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format, int group,
-                       void* Y, int y_dtype, void* workspace, size_t workspace_bytes, const MmWait& wait, void* stream) {
+                       void* Y, int y_dtype, void* workspace, size_t workspace_bytes, const MmWait& wait, dq_matmul_info* info,
+                       void* stream) {
   if (tokens <= 0 || rows <= 0 || cols <= 0 || group <= 0 || cols % group != 0) return DQ_EINVAL;
   if (format < DQ_INT4 || format > DQ_MXFP8) return DQ_EINVAL;
   if (format != DQ_NVFP4 && format != DQ_MXFP4 && format != DQ_MXFP8) return DQ_EUNSUPPORTED;
@@ -1230,13 +1251,13 @@ static int matmul_call(const dq_outputs* X, int64_t tokens, const dq_outputs* W,
   p.N = rows;
   p.K = cols;
   p.flags = workspace ? &static_cast<WsHeader*>(workspace)->flags : nullptr;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int dev = 0, sms = 0;
+  MmCall c{0, static_cast<cudaStream_t>(stream), wait, info};
+  int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DQ_ECUDA;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DQ_ECUDA;
-  const cudaError_t e = format == DQ_NVFP4   ? matmul_fmt<FMT_NVFP4>(p, wait, sms, s)
-                        : format == DQ_MXFP4 ? matmul_fmt<FMT_MXFP4>(p, wait, sms, s)
-                                             : matmul_fmt<FMT_MXFP8>(p, wait, sms, s);
+  if (cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return DQ_ECUDA;
+  const cudaError_t e = format == DQ_NVFP4   ? matmul_fmt<FMT_NVFP4>(p, c)
+                        : format == DQ_MXFP4 ? matmul_fmt<FMT_MXFP4>(p, c)
+                                             : matmul_fmt<FMT_MXFP8>(p, c);
   return e == cudaSuccess ? DQ_OK : DQ_ECUDA;
 }
 
@@ -1245,7 +1266,7 @@ static int matmul_call(const dq_outputs* X, int64_t tokens, const dq_outputs* W,
 extern "C" int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format,
                          int group, void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
   return dq::matmul_call(X, tokens, W, rows, cols, format, group, Y, y_dtype, workspace, workspace_bytes, dq::MmWait(),
-                         stream);
+                         nullptr, stream);
 }
 
 extern "C" int dq_matmul_selftest(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols,
@@ -1258,5 +1279,12 @@ extern "C" int dq_matmul_selftest(const dq_outputs* X, int64_t tokens, const dq_
   wait.limit_ns = wait_ns;
   wait.stop = dq::stop_key(rank, role) << dq::kStopAtBits | at;
   return dq::matmul_call(X, tokens, W, rows, cols, format, group, Y, y_dtype, workspace, workspace_bytes,
-                         wait, stream);
+                         wait, nullptr, stream);
+}
+
+extern "C" int dq_matmul_kernel(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols,
+                                int format, int group, const void* Y, int y_dtype, dq_matmul_info* info) {
+  if (!info) return DQ_EINVAL;
+  return dq::matmul_call(X, tokens, W, rows, cols, format, group, const_cast<void*>(Y), y_dtype, nullptr, 0, dq::MmWait(), info,
+                         nullptr);
 }

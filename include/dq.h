@@ -330,6 +330,21 @@ int dq_act_quant(const void* X, int x_dtype, int64_t rows, int64_t cols, const v
 int dq_matmul(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format, int group,
               void* Y, int y_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Which kernel a dq_matmul with these arguments runs on the current device, and
+ * how it divides the work (for tests and measurements; nothing is enqueued and no
+ * operand is read). */
+enum { DQ_MATMUL_ANY = 0, DQ_MATMUL_TILE = 1, DQ_MATMUL_PAIR = 2 };
+typedef struct {
+  int kernel;           /* DQ_MATMUL_ANY: codes of any alignment; _TILE: a CTA a tile; _PAIR: a pair of CTAs a tile */
+  int tile_tokens;      /* tokens of a tile */
+  int aligned_scales;   /* the variant for rows of scales at multiples of 16 bytes */
+  int64_t whole_tiles;  /* tiles whose columns one CTA, or one pair, sums */
+  int64_t split_tiles;  /* tiles whose columns the CTAs, or pairs, of a cluster share */
+  int split;            /* ... how many of them */
+} dq_matmul_info;
+int dq_matmul_kernel(const dq_outputs* X, int64_t tokens, const dq_outputs* W, int64_t rows, int64_t cols, int format,
+                     int group, const void* Y, int y_dtype, dq_matmul_info* info);
+
 /* Self-test of dq_matmul's bounded device waits (no counterpart in the method;
  * failure detection): dq_matmul with waits of wait_ns (10^6 .. 10^9, instead of
  * a second) in which one role of the CTA `rank` (0 .. 7) of every cluster stops as if its
