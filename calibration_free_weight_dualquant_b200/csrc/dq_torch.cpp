@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -169,14 +170,13 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& f) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
     return nullptr;
   }
+  HANDLE_TH_ERRORS  // torch's exceptions as torch raises them: an allocation that failed is its OutOfMemoryError
   try {
     return f();
   } catch (const Fail&) {
     return nullptr;
-  } catch (const std::exception& e) {  // an allocation that failed
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
   }
+  END_HANDLE_TH_ERRORS
 }
 
 // matmul(stream, X, W, format, out, out_dtype, workspace, check) -> Y
