@@ -16,9 +16,10 @@ from typing import Optional
 
 import torch
 
+from . import build
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libdq.so")
-MARSHAL_PATH = os.path.join(_PKG, "lib", "_dq_torch.so")
 
 STATUS = {0: "DQ_OK", 1: "DQ_EINVAL", 2: "DQ_EUNSUPPORTED", 3: "DQ_EWORKSPACE", 4: "DQ_ENONFINITE", 5: "DQ_ECUDA"}
 
@@ -139,14 +140,15 @@ _marshal = None
 
 
 def load_marshal():
-    """Load the compiled marshalling of the linear layer's calls (built in-tree by ``build.py``); raise if it is
-    missing."""
+    """Load the compiled marshalling of the linear layer's calls (built in-tree by ``build.py``); raise if the one for
+    this Python and this torch is missing."""
     global _marshal
     if _marshal is None:
         load_library()
-        if not os.path.exists(MARSHAL_PATH):
-            raise DQError(5, "load_marshal: %s is not built (run __graft_entry__.build())" % MARSHAL_PATH)
-        spec = importlib.util.spec_from_file_location("_dq_torch", MARSHAL_PATH)
+        path = build.marshal_path()
+        if not os.path.exists(path):
+            raise DQError(5, "load_marshal: %s is not built (run __graft_entry__.build())" % path)
+        spec = importlib.util.spec_from_file_location("_dq_torch", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         m.set_error(DQError)

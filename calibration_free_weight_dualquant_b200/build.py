@@ -1,4 +1,5 @@
-"""Build libdq.so in-tree with nvcc for sm_100a, and _dq_torch.so (argument marshalling) with the host compiler.
+"""Build libdq.so in-tree with nvcc for sm_100a, and _dq_torch.*.so (argument marshalling) with the
+host compiler.
 
     python -m calibration_free_weight_dualquant_b200.build
 """
@@ -17,7 +18,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(OUT_DIR, "libdq.so")
-MARSHAL = os.path.join(OUT_DIR, "_dq_torch.so")
 MARSHAL_SOURCE = os.path.join(CSRC, "dq_torch.cpp")
 SOURCES = ["dq_capi.cu", "dq_solver.cu", "dq_static.cu", "dq_act.cu", "dq_norm.cu", "dq_matmul.cu"]
 HEADERS = ["dq_device.cuh", "dq_fast.cuh", "dq_init.cuh", "dq_internal.h", "dq_iter.cuh", "dq_launch.h",
@@ -51,25 +51,35 @@ def _run(cmd, what: str) -> str:
     return r.stdout + r.stderr
 
 
+def marshal_path() -> str:
+    """Where the compiled marshalling for this interpreter and this torch belongs: its name holds their binary
+    interfaces, so a module built against others is neither kept nor loaded."""
+    import torch
+    name = "_dq_torch.%s-torch%s-abi%d.so" % (sysconfig.get_config_var("SOABI"), torch.__version__,
+                                              torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(OUT_DIR, name)
+
+
 def build_marshal(force: bool = False) -> str:
     """The CPython module of csrc/dq_torch.cpp, against torch's headers and libdq.so."""
-    deps = [MARSHAL_SOURCE, os.path.join(INCLUDE, "dq.h")]
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
-        return MARSHAL
     import torch
+    path = marshal_path()
+    deps = [MARSHAL_SOURCE, os.path.join(INCLUDE, "dq.h")]
+    if not force and os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps):
+        return path
     t = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     includes = [sysconfig.get_paths()["include"], os.path.join(t, "include"),
                 os.path.join(t, "include", "torch", "csrc", "api", "include"), cuda, INCLUDE]
-    tmp = MARSHAL + ".tmp%d" % os.getpid()
+    tmp = path + ".tmp%d" % os.getpid()
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC"]
     cmd += [a for d in includes for a in ("-I", d)]
     cmd += ["-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, MARSHAL_SOURCE, "-o", tmp, "-L", OUT_DIR,
             "-l:libdq.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(t, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_cuda",
             "-ltorch_python"]
     _run(cmd, "g++ on dq_torch.cpp")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
