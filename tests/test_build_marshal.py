@@ -55,3 +55,27 @@ def test_loading_one_of_another_torch_is_refused(monkeypatch):
     with pytest.raises(binding.DQError) as e:
         binding.load_marshal()
     assert e.value.status == 5 and "not built" in str(e.value)
+
+
+def test_the_library_is_built_where_the_module_cannot_be(tmp_path, monkeypatch):
+    """No Python headers, say: the solver is built and stays usable, the linear layer's calls say what is missing."""
+    def run(cmd, what):
+        if "dq_torch" in what:
+            raise RuntimeError(what + " failed")
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write(what)
+        return ""
+
+    monkeypatch.setattr(build, "OUT_DIR", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", str(tmp_path / "libdq.so"))
+    monkeypatch.setattr(build, "MARSHAL", str(tmp_path / "_dq_torch.so"), raising=False)
+    monkeypatch.setattr(build, "_run", run)
+    with pytest.warns(UserWarning, match="linear layer"):
+        assert build.build() == str(tmp_path / "libdq.so")
+    assert os.path.exists(tmp_path / "libdq.so")
+    with pytest.raises(RuntimeError):
+        build.build_marshal()
+    monkeypatch.setattr(binding, "_marshal", None)
+    with pytest.raises(binding.DQError) as e:
+        binding.load_marshal()
+    assert e.value.status == 5 and "not built" in str(e.value)
