@@ -4,8 +4,8 @@
 //   Y[t][n] = s_x s_w sum_k (a_x[t][k/G] q_x[t][k]) (a_w[n][k/G] q_w[n][k])
 //
 // (DualQuant arXiv 2610.13767 summary, section 4.4: X W^T = (X D_b) Q^T D_a;
-// the column scales b are in q_x already).  Sums are held in fp32 and rounded
-// once, after the tensor scales, to the output type.
+// the column scales b are in q_x already).  Sums are held in fp32, multiplied by
+// the tensor scales in fp32 and rounded once more, to the output type.
 #include <climits>
 
 #include <cuda.h>
@@ -105,10 +105,11 @@ __device__ __forceinline__ float code_value(const unsigned char* q, int64_t at) 
 // Any shape and alignment: a 64 x 64 tile of Y per CTA, 16-column slices of
 // both operands' codes decoded to fp32 in shared memory, 4 x 4 outputs per
 // thread.  A slice lies within one block of each operand, so its sum of code
-// products (exact: 16 products of at most 18 significant bits) is multiplied
-// by the two block scales at once; powers of two add their exponents, so that
-// scales at the ends of their range do not overflow on the way.  Bound by
-// fp32 arithmetic and the decoding: 200 x 400 x 400 NVFP4 86 us (0.7 TFLOP/s).
+// products (exact for E2M1, whose products are multiples of 1/4 up to 36; fp32
+// additions for E4M3) is multiplied by the two block scales at once; powers of
+// two add their exponents, so that scales at the ends of their range do not
+// overflow on the way.  Bound by fp32 arithmetic and the decoding:
+// 200 x 400 x 400 NVFP4 87 us (0.7 TFLOP/s).
 // Taken only where the copies of the tensor-core kernels cannot read the codes:
 // rows of codes that do not start at multiples of 16 bytes (a 4-bit row length that
 // is not a multiple of 32, or such an address).
@@ -187,9 +188,9 @@ __global__ void __launch_bounds__(256) k_matmul_any(MatmulProblem p) {
 //
 // Up to 64 tokens the weight's bytes bound it, and below some 30 MB the fixed 3.5
 // us of a tile's start, join and store.  1 token (GPU time): NVFP4 28672 x 4096
-// 15.4 us = 4.3 TB/s, 4096 x 4096 5.2 us (1.8 TB/s); MXFP8 4096 x 14336 13.0 us =
-// 4.7 TB/s.  16 tokens MXFP4 4096 x 14336: 7.9 us = 4.0 TB/s.  More tokens, as long
-// as the tiles are few (tc_ns): 64 or 128 a tile; 1000 x 1001 x 1056 NVFP4 7.1 us,
+// 15.2 us = 4.3 TB/s, 4096 x 4096 5.4 us (1.8 TB/s); MXFP8 4096 x 14336 13.1 us =
+// 4.6 TB/s.  16 tokens MXFP4 4096 x 14336: 8.1 us = 3.9 TB/s.  More tokens, as long
+// as the tiles are few (tc_ns): 64 or 128 a tile; 1000 x 1001 x 1056 NVFP4 7.2 us,
 // 12.1 with pairs of CTAs.
 //
 // Warps: 0 issues the copies, 1 the tensor-core work; 2 and 4 bring the
@@ -421,8 +422,8 @@ __device__ __forceinline__ bool scale_warp(int unit, ScaleTurn& t, int tiles_per
                                            int block_bytes, uint64_t* full, uint64_t* empty, unsigned limit_ns, unsigned* flags,
                                            unsigned stop, uint32_t leader) {
 #define DQ_SCALE_LOOP(U) \
-  scale_loop<PAIR, SLOTS, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty, limit_ns, flags, stop, \
-                         leader)
+  scale_loop<PAIR, SLOTS, U>(t, tiles_per_piece, s, row0, rows, nb, k0, n, ring, slot_bytes, block_bytes, full, empty,   \
+                             limit_ns, flags, stop, leader)
   if (WIDE) return unit == 32 ? DQ_SCALE_LOOP(32) : DQ_SCALE_LOOP(16);
   return unit >= 8 ? DQ_SCALE_LOOP(8) : DQ_SCALE_LOOP(1);
 #undef DQ_SCALE_LOOP
@@ -439,7 +440,8 @@ struct MmLaunch {
 
 template <int FMT, int BN, bool WIDE>
 __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
-    k_matmul_tc(const __grid_constant__ MatmulProblem p, const __grid_constant__ MmLaunch l, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
+    k_matmul_tc(const __grid_constant__ MatmulProblem p, const __grid_constant__ MmLaunch l,
+                const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
   using G = MmGeo<FMT, BN>;
   using F = TcFormat<FMT>;
   extern __shared__ unsigned char mm_smem[];
@@ -646,11 +648,14 @@ __global__ void __launch_bounds__(kMmThreads, WIDE ? 3 : 2)
 // into registers, rounded to the output type and released before it is stored,
 // so the next tile's multiply-adds wait for the tensor-memory reads alone.
 //
-// MXFP8 is bound by the tensor cores (the pipe is active 89 % of the time) and the
-// last wave: 4096 x 4096 x 14336 180 us = 2.7 PFLOP/s.  NVFP4 and MXFP4 do the
-// multiply-adds of the same bytes in half the time and are bound by what feeds
-// them: operands from L2 (9 TB/s) and the scales.  NVFP4 8192 x 14336 x 4096 215 us =
-// 4.5 PFLOP/s, MXFP4 8192 x 4096 x 4096 56 us = 4.9 PFLOP/s.
+// MXFP8 is bound by the tensor cores (the pipe is active 90 % of the time) and the
+// last wave: 4096 x 4096 x 14336 181 us = 2.7 PFLOP/s.  NVFP4 and MXFP4 do the
+// multiply-adds of the same bytes in half the time, and no unit is at its limit (NVFP4:
+// tensor pipe 60 %, shared memory and L1 66 %, L2 41 %): between them stand
+// the scales' way through shared memory and the wait of a tile's first multiply-adds
+// for the reading of the tile before (two accumulators of 256 columns and the scales
+// are more than tensor memory has).  NVFP4 8192 x 14336 x 4096 218 us = 4.4 PFLOP/s, MXFP4 8192 x 4096 x 4096
+// 57 us = 4.8 PFLOP/s.  The 16-bit outputs of NVFP4 spill 16 bytes a thread.
 constexpr int kPairThreads = 16 * 32;
 constexpr int kPairEpilogue = 8;  // warps
 constexpr int kPairStages = 5;
@@ -1187,10 +1192,11 @@ static cudaError_t matmul_pair(const MatmulProblem& p, const MmCall& c) {
 // part, with the join of split tiles, and the K tiles that a CTA works on, each the
 // time that its SM's operands take to arrive, whichever the kernel (measured: 70
 // bytes a ns with a scale per 16, 90 with one per 32).  Chosen by this, the kernel
-// was within 10 % of the fastest of the three in nearly all of 270 products of 65 to
-// 1500 tokens; the pairs for all of them took up to 1.7 times as long (192 x 4096 x
-// 1024 NVFP4: 64 tokens a tile 5.3 us, 128 8.2, pairs 6.9; 128 x 4096 x 14336: 15.9,
-// 12.9 and 16.9; 300 x 4096 x 14336: 34.4, 25.3 and 20.5).
+// was within 10 % of the fastest of the three in 260 of 264 products of 65 to 1500
+// tokens, 17 % off at worst and 0.7 % on average; the pairs for all of them took 1.22
+// times as long on average, 1.83 times at most (192 x 4096 x 1024 NVFP4: 64 tokens a tile
+// 5.3 us, 128 8.2, pairs 6.9; 128 x 4096 x 14336: 15.9, 12.9 and 16.9; 300 x 4096 x
+// 14336: 34.4, 25.3 and 20.5).
 constexpr int tile_ns(int fmt, int bn) { return (128 + bn) * 128 / (fmt == FMT_NVFP4 ? 70 : 90); }
 static int64_t tc_ns(const MatmulProblem& p, int fmt, int64_t nk, int bn, int sms) {
   const int64_t tiles = (p.N + 127) / 128 * ((p.T + bn - 1) / bn);

@@ -505,9 +505,12 @@ __device__ __forceinline__ unsigned long long amax_finish(const RowProblem& p, A
 // between the sum of squares and the quantization (NC 0: rows of more than 2048
 // chunks, read twice).  The sum is in fp64: x' has to be known to 2^-20 and
 // decided exactly where that is not enough, and one fp64 add an element is 7 % of
-// that pipe.  8192 x 4096 MXFP8 with residual: 50 us, 4.7 TB/s of the 7 bytes an
-// element; 1 x 4096: 3.8 us.  Bound by the latency of a row's loads and its two
-// barriers, with the issue slots half used.
+// that pipe.  8192 x 4096 with residual: MXFP8 50 us, 4.7 TB/s of the 7 bytes an
+// element; MXFP4 44 us; NVFP4, which writes h, meets the grid and reads h again, 96 us.
+// 1 x 4096 MXFP8: 4 us.  Bound by the latency of a row's loads and its two
+// barriers, with the issue slots half used.  Spilled, bytes stored a thread, bf16 and
+// fp16 inputs: NC 2 (held to 80 registers) MXFP8 40 and 114, MXFP4 36 and 110, NVFP4
+// 270 and 270; NC 4 (128) MXFP8 0 and 174, MXFP4 0 and 166, NVFP4 34 and 34; others none.
 __host__ __device__ constexpr int norm_threads(int nc) { return nc == 1 || nc == 4 ? 512 : 256; }
 
 template <int FMT, int XDT, int NC>
@@ -745,7 +748,8 @@ __device__ __forceinline__ void glu_fast16(const V16& gv, const V16& uv, const G
 
 // A warp takes 512 columns of a row at a time, two such items in turn, so that one's
 // loads are under way while the other is computed.  8192 x 14336 MXFP8: 114 us, 5.2
-// TB/s of the 5 bytes an element; 16 x 14336: 4.7 us.  Bound by instructions (22 an
+// TB/s of the 5 bytes an element; MXFP4 105 us; NVFP4, which reads and computes twice,
+// 211 us.  16 x 14336 MXFP8: 4.7 us.  Bound by instructions (22 an
 // element: the sigmoid's exponential and reciprocal, two conversions of the
 // bracket's ends); a ring of asynchronous copies added to them: 168 us against the
 // 133 of its time.
@@ -865,8 +869,8 @@ static cudaError_t row_launch(void (*kern)(RowProblem), const RowProblem& p, boo
 }
 
 // Few rows: a chunk a thread, for latency.  From 4 rows an SM on: 2 chunks a
-// thread at 80 registers, for 24 warps an SM (8192 x 4096 MXFP8: 53 us with 1
-// chunk a thread, 50 with 2, 51 with 4 at 126 registers).  What bounds it then is
+// thread at 80 registers and their spills, for 24 warps an SM (8192 x 4096 MXFP8: 53 us
+// with 1 chunk a thread, 50 with 2, 51 with 4 at 126 registers).  What bounds it then is
 // latency, not the memory: bringing the next row into shared memory meanwhile
 // took longer (56 us).
 template <int FMT, int XDT>

@@ -13,8 +13,8 @@
  * after each update, scale 1 for an all-zero code slice) and by the DualQuant
  * (arXiv 2610.13767) summary (§3 formats, §4.3 BCD, App. B closed forms).
  * It also runs the linear layer that such weights are for: dq_matmul multiplies
- * them by quantized activations, which dq_act_quant, dq_norm_quant and
- * dq_glu_quant make.
+ * them by quantized activations, which dq_norm_quant and dq_glu_quant make in
+ * DQ_NVFP4, DQ_MXFP4 and DQ_MXFP8, and dq_act_quant in the two 4-bit ones.
  *
  * Conventions shared by every entry point
  *  - All tensor pointers are DEVICE pointers unless the name says host; the
@@ -306,7 +306,7 @@ int dq_act_quant(const void* X, int x_dtype, int64_t rows, int64_t cols, const v
 
 /* The product of quantized activations and a quantized weight matrix
  * (DualQuant summary §4.4: X W^T = (X D_b) Q^T D_a, with b folded into the
- * activations by dq_act_quant, dq_norm_quant or dq_glu_quant):
+ * activations by dq_norm_quant, dq_glu_quant or, in the 4-bit formats, dq_act_quant):
  *   Y[t][n] = s_x s_w sum_k (a_x q_x)[t][k] (a_w q_w)[n][k]
  * X  codes [tokens][..] and block_scales [tokens][cols/group] of the
  *    activations, W those of the weights [rows][cols] (a dq_solve or dq_rtn
@@ -316,10 +316,19 @@ int dq_act_quant(const void* X, int x_dtype, int64_t rows, int64_t cols, const v
  *    not overlap the operands.
  * Formats DQ_NVFP4, DQ_MXFP4 and DQ_MXFP8; the integer grids return
  * DQ_EUNSUPPORTED.  cols is a multiple of the group and at most
- * 2^27, the other sizes are any from 1.  Products of codes and scales are exact, sums are fp32 and rounded
- * once to y_dtype; a value beyond its range becomes an infinity.  A NaN block
- * scale (E8M0 0xFF, E4M3 0x7F) makes its row's outputs NaN and no others.  The
- * order of a sum depends on the shape alone, so equal calls give equal bits.
+ * 2^27, the other sizes are any from 1.  Products of codes and scales are exact.
+ * Sums are fp32: 32 columns (DQ_MXFP8) or 64 at a time are added to the sum so
+ * far, each time off in fp32's last place, the sum is multiplied by the tensor
+ * scales in fp32, and that is rounded once to y_dtype; a value beyond its range
+ * becomes an infinity.  A caller of the fp32 output should know that these errors
+ * add up in proportion to the columns: measured, relative to
+ * sqrt(sum (x w)^2), an RMS of 4e-6 (DQ_MXFP8), 3e-6 (DQ_NVFP4) and 1e-6
+ * (DQ_MXFP4) at 14336 columns, 4e-5 (DQ_MXFP8) at 131072.  A NaN block
+ * scale (E8M0 0xFF, E4M3 0x7F) makes its row's outputs NaN and no others.
+ * Equal calls give equal bits where the sizes, the format, y_dtype, the device
+ * (and how many of its SMs the context may use) and the alignment of codes and
+ * block scales are equal: they choose the kernel, the split of the columns and
+ * so the order of a sum.
  * Codes that are 16-byte aligned in every row (16-byte aligned pointers and,
  * in the 4-bit formats, cols a multiple of 32) take the tensor-core kernels;
  * others take a slower kernel.

@@ -119,6 +119,28 @@ def test_random_operands(size, fmt, kernel):
         assert not off.any(), "%s: %d of %d" % (dt, off.sum().item(), off.numel())
 
 
+LONG = [r for r in RUNS if r[0][2] >= 4096]
+
+
+@pytest.mark.parametrize("size,fmt,kernel", LONG, ids=["%s-%dx%dx%d+%d" % (f, *size) for size, f, _ in LONG])
+def test_rms_error_of_long_fp32_sums(size, fmt, kernel):
+    """RMS error over sqrt(sum (x w)^2), the RMS of a sum of random signs.  The tensor core adds the products of 32
+    (MXFP8) or 64 columns at a time to an fp32 sum; each addition is off by at most a unit of the last place, 2^-23 of a
+    partial sum, whose RMS the whole one's bounds, and in the worst case all of them in one direction.  Two products
+    with the tensor scales, and what is within an addition, one unit more, are 4 2^-24 together.  A partial sum in
+    fp16 or bf16 would be off by about 2^-13 or 2^-10 of it: eight times
+    the bound at 4096 columns and twice at 14336."""
+    tokens, rows, cols, shift = size
+    x = on_device(ref.random_quantized(tokens, cols, fmt, tokens + cols + 1), shift)
+    w = on_device(ref.random_quantized(rows, cols, fmt, rows + cols + 1), shift)
+    s = ref.tensor_scale(x, fmt) * ref.tensor_scale(w, fmt)
+    xv, wv = values(x, fmt), values(w, fmt)
+    y = binding.dq_matmul(x, w, fmt, out_dtype=torch.float32).double()
+    error = (y - (xv @ wv.T) * s) / (((xv * xv) @ (wv * wv).T).sqrt() * s)
+    additions = -(-cols // (32 if fmt == "mxfp8" else 64))
+    assert error.square().mean().sqrt().item() <= additions * 2.0 ** -23 + 4 * 2.0 ** -24
+
+
 def integers(rows: int, cols: int, fmt: str, seed: int, exps):
     """(quantized matrix, integer values, scale exponent of each row)."""
     rng = torch.Generator().manual_seed(seed)
